@@ -12,7 +12,7 @@ import ctypes as C
 
 from . import _binding as B
 from ._binding import (DTYPE_BF16, DTYPE_F16, EPI_F16, EPI_F32, EPI_RESID, EPI_SWIGLU, SEG_IMAGE,  # noqa: F401
-                       SEG_TEXT, Geom, Qi21Error,
+                       SEG_TEXT, Geom, Qi21Error, Rope, rope,
                        CLASSES, check, device_status, exported_symbols, profile_enable, profile_read, geom, layer_plane_bytes, layout_indices,
                        layout_rows, load, workspace_bytes)
 
@@ -22,6 +22,7 @@ __all__ = [
     "timestep_mods", "denoise", "set_checks", "PackedLayerFp8", "pack_layer_fp8", "workspace_bytes_fp8",
     "prefill_fp8", "step_batch_fp8", "op_quant_rows", "op_rowop_fp8", "op_gemm_fp8", "Graph", "graph_step_batch", "graph_step_batch_fp8", "graph_denoise_batch", "count_nonfinite", "CHECK_FINITE", "CHECK_AMAX", "AMAX_SITES", "amax_read", "denoise_batch", "device_status", "selftest_wait_timeout", "build",
     "profile_enable", "profile_read", "CLASSES", "op_rowop", "op_mods_prep", "op_gemm", "op_gemm_split", "op_qkrope", "op_kvcopy", "op_attention",
+    "Rope", "rope", "op_rope", "PagedKV", "op_kv_append", "attention_paged_bytes", "op_attention_paged",
 ]
 
 
@@ -493,6 +494,152 @@ def op_attention(panel, heads, out, nq, n_own, kv_pre=None, n_pre=0, vis=None, s
                                    _ptr(kv_pre, panel.dtype, "kv_pre"), n_pre, n_own,
                                    _ptr(vis, torch.int32, "vis"), _ptr(out, panel.dtype, "out"),
                                    _stream(stream)))
+
+
+# ------------------------------------------------------- paged K/V cache ----
+
+def _here(t, name):
+    """Refuse a tensor of another device than the current one (pointers are
+    taken on the current device)."""
+    torch = _torch()
+    if not isinstance(t, torch.Tensor) or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    if t.device.index != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
+    return t
+
+
+def _heads_view(t, dim, name):
+    """(pointer, row stride) of a [rows, heads, dim] tensor whose rows may
+    lie apart and whose heads are dense."""
+    _here(t, name)
+    if t.dim() != 3 or t.shape[2] != dim:
+        raise ValueError(f"{name} must be [rows, heads, {dim}], got {tuple(t.shape)}")
+    wide = t.shape[1] * dim
+    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
+        raise ValueError(f"{name}: the heads of a row must be dense")
+    if t.shape[0] > 1 and t.stride(0) < wide:
+        raise ValueError(f"{name}: rows overlap")
+    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else wide
+
+
+def _flat(t, dtype, n, name):
+    """Pointer of a contiguous tensor of n elements on the current device."""
+    if t is None:
+        return None
+    _here(t, name)
+    if t.numel() != n:
+        raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
+    return _ptr(t, dtype, name)
+
+
+def _elem(t):
+    torch = _torch()
+    e = {torch.float32: B.ELEM_F32, torch.float16: B.ELEM_F16, torch.bfloat16: B.ELEM_BF16}.get(t.dtype)
+    if e is None:
+        raise TypeError(f"expected an f32, f16 or bf16 tensor, got {t.dtype}")
+    return e
+
+
+def op_rope(r: Rope, x, pos, out=None, grad=False, stream=None):
+    """qi21_op_rope: x [rows, heads, head_dim] (f32, f16 or bf16; rows may
+    lie apart, as in a panel) turned by pos (int64 [rows], or [rows, 3] with
+    three axes) into out (None: in place); grad=True turns a gradient back.
+    Returns the output."""
+    torch = _torch()
+    px, ldx = _heads_view(x, r.head_dim, "x")
+    if out is None:
+        out = x
+    po, ldo = _heads_view(out, r.head_dim, "out")
+    if out.shape != x.shape or out.dtype != x.dtype:
+        raise ValueError("out must have x's shape and dtype")
+    if x.shape[1] == 0:
+        return out
+    check(load().qi21_op_rope(C.byref(r), _elem(x), x.shape[0], x.shape[1], px, ldx, po, ldo,
+                              _flat(pos, torch.int64, x.shape[0] * r.naxes, "pos"), 1 if grad else 0,
+                              _stream(stream)))
+    return out
+
+
+class PagedKV:
+    """A batch over a paged cache (qi21_paged): pool [npages, page_rows, 2,
+    kv_heads, head_dim] (f16 or bf16), table int32 [nseq, pages], lens int32
+    [nseq] (own rows, the call's among them), cu int32 [nseq + 1], and the
+    prefix that all sequences share as prefix_pages int32 and prefix_len.
+    Keeps the tensors alive; their contents are read when the work runs."""
+
+    def __init__(self, pool, table, lens, cu, prefix_pages=None, prefix_len=0):
+        torch = _torch()
+        _here(pool, "pool")
+        if pool.dim() != 5 or pool.shape[2] != 2:
+            raise ValueError(f"pool must be [npages, page_rows, 2, kv_heads, head_dim], got {tuple(pool.shape)}")
+        if table.dim() != 2:
+            raise ValueError("table must be [nseq, pages]")
+        nseq, stride = table.shape
+        c = B.Paged()
+        c.dtype = _dt_code(pool)
+        c.pool = _ptr(pool, pool.dtype, "pool")
+        c.npages, c.page_rows, _, c.kv_heads, c.head_dim = pool.shape
+        c.nseq, c.table_stride = nseq, stride
+        c.table = _flat(table, torch.int32, nseq * stride, "table")
+        c.lens = _flat(lens, torch.int32, nseq, "lens")
+        c.cu = _flat(cu, torch.int32, nseq + 1, "cu")
+        c.prefix_len = prefix_len
+        if prefix_len > 0:
+            if prefix_pages is None:
+                raise ValueError("prefix_len without prefix_pages")
+            need = -(-prefix_len // c.page_rows) if c.page_rows else 0
+            if prefix_pages.numel() < need:
+                raise ValueError(f"prefix_pages must have {need} entries, got {prefix_pages.numel()}")
+            c.prefix_pages = _flat(prefix_pages, torch.int32, prefix_pages.numel(), "prefix_pages")
+        self.c = c
+        self._keep = (pool, table, lens, cu, prefix_pages)
+
+
+def op_kv_append(kv: PagedKV, k, v, rope=None, pos=None, stream=None):
+    """qi21_op_kv_append: new keys (turned by rope at pos, int64; None: the
+    rows' places in their sequences) and values, each [rows, kv_heads,
+    head_dim], to their pages."""
+    torch = _torch()
+    c = kv.c
+    pk, ldk = _heads_view(k, c.head_dim, "k")
+    pv, ldv = _heads_view(v, c.head_dim, "v")
+    if k.shape != v.shape or k.shape[1] != c.kv_heads:
+        raise ValueError(f"k and v must be [rows, {c.kv_heads}, {c.head_dim}]")
+    if _dt_code(k) != c.dtype or _dt_code(v) != c.dtype:
+        raise TypeError("k and v must have the pool's dtype")
+    n = k.shape[0] * (rope.naxes if rope is not None else 1)
+    check(load().qi21_op_kv_append(C.byref(c), k.shape[0], pk, ldk, pv, ldv, C.byref(rope) if rope is not None else None,
+                                   _flat(pos, torch.int64, n, "pos"), _stream(stream)))
+
+
+def attention_paged_bytes(kv: PagedKV, rows: int, heads: int) -> int:
+    """qi21_attention_paged_bytes: workspace of up to `rows` query rows."""
+    n = int(load().qi21_attention_paged_bytes(C.byref(kv.c), rows, heads))
+    if n == 0:
+        raise Qi21Error(-2, load().qi21_last_error().decode())
+    return n
+
+
+def op_attention_paged(kv: PagedKV, q, out, workspace, causal=True, vis=None, scale=None, stream=None):
+    """qi21_op_attention_paged: query rows q [rows, heads, head_dim] over
+    [prefix, own rows] of their sequences into out; scale defaults to
+    1 / sqrt(head_dim). vis int32 [rows] (read as unsigned): leading runs in
+    place of the causal ones."""
+    torch = _torch()
+    c = kv.c
+    pq, ldq = _heads_view(q, c.head_dim, "q")
+    po, ldo = _heads_view(out, c.head_dim, "out")
+    if out.shape != q.shape:
+        raise ValueError("out must have q's shape")
+    if _dt_code(q) != c.dtype or _dt_code(out) != c.dtype:
+        raise TypeError("q and out must have the pool's dtype")
+    _here(workspace, "workspace")
+    check(load().qi21_op_attention_paged(C.byref(c), q.shape[0], q.shape[1], pq, ldq, po, ldo, 1 if causal else 0,
+                                         _flat(vis, torch.int32, q.shape[0], "vis"),
+                                         c.head_dim ** -0.5 if scale is None else scale,
+                                         _ptr(workspace, None, "workspace"),
+                                         workspace.numel() * workspace.element_size(), _stream(stream)))
 
 
 def selftest_wait_timeout(stream=None):

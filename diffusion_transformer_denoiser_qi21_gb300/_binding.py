@@ -26,6 +26,8 @@ SEG_TEXT = 0
 SEG_IMAGE = 1
 EPI_F16, EPI_F32, EPI_RESID, EPI_SWIGLU = 0, 1, 2, 3
 DTYPE_F16, DTYPE_BF16 = 0, 1
+ROPE_LAYOUTS = {"interleaved": 0, "half": 1}
+ROPE_SCALINGS = {"plain": 0, "linear": 1, "base": 2, "ramp": 3, "band": 4}
 ELEM_F16, ELEM_BF16, ELEM_F32 = 2, 3, 4
 
 
@@ -56,10 +58,24 @@ class Layer(C.Structure):
                 ("norm_q", C.c_void_p), ("norm_k", C.c_void_p)]
 
 
+class Rope(C.Structure):
+    _fields_ = [("head_dim", C.c_int32), ("rot_dim", C.c_int32), ("layout", C.c_int32), ("naxes", C.c_int32),
+                ("out_scale", C.c_float), ("axis", C.c_uint8 * 128), ("turns", C.c_uint64 * 128)]
+
+
+class Paged(C.Structure):
+    _fields_ = [("pool", C.c_void_p), ("dtype", C.c_int32), ("npages", C.c_int32), ("page_rows", C.c_int32),
+                ("kv_heads", C.c_int32), ("head_dim", C.c_int32), ("nseq", C.c_int32), ("table", C.c_void_p),
+                ("table_stride", C.c_int32), ("lens", C.c_void_p), ("cu", C.c_void_p),
+                ("prefix_pages", C.c_void_p), ("prefix_len", C.c_int32)]
+
+
 _vp = C.c_void_p
 _i32 = C.c_int32
 _sz = C.c_size_t
 _f = C.c_float
+_i64 = C.c_int64
+_d = C.c_double
 
 # name -> (restype, argtypes)
 _SIGS = {
@@ -117,6 +133,12 @@ _SIGS = {
     "qi21_op_qkrope": (C.c_int, [_i32, _i32, _i32, _f, _vp, _vp, _vp, _vp, _vp, _vp]),
     "qi21_op_kvcopy": (C.c_int, [_i32, _i32, _vp, _vp, _vp]),
     "qi21_op_attention": (C.c_int, [_i32, _i32, _i32, _vp, _vp, _i32, _i32, _vp, _vp, _vp]),
+    "qi21_rope_init": (C.c_int, [C.POINTER(Rope), _i32, _i32, _i32, C.POINTER(_i32), _d, _i32, _d, _d, _d, _d, _d]),
+    "qi21_op_rope": (C.c_int, [C.POINTER(Rope), _i32, _i32, _i32, _vp, _i64, _vp, _i64, _vp, _i32, _vp]),
+    "qi21_op_kv_append": (C.c_int, [C.POINTER(Paged), _i32, _vp, _i64, _vp, _i64, C.POINTER(Rope), _vp, _vp]),
+    "qi21_attention_paged_bytes": (_sz, [C.POINTER(Paged), _i32, _i32]),
+    "qi21_op_attention_paged": (C.c_int, [C.POINTER(Paged), _i32, _i32, _vp, _i64, _vp, _i64, _i32, _vp, _f, _vp, _sz,
+                                          _vp]),
 }
 
 _lib = None
@@ -159,6 +181,25 @@ def geom(dim, heads, mlp_hidden, layers, axes=(16, 56, 56), eps=1e-6, theta=1000
     g.eps, g.theta = eps, theta
     g.dtype = dtype
     return g
+
+
+def rope(head_dim, rot_dim=None, layout="interleaved", axes=None, base=10000.0, scaling="plain", factor=1.0,
+         orig_len=0.0, fast_turns=0.0, slow_turns=0.0, out_scale=0.0) -> Rope:
+    """qi21_rope_init: a rotation of the first rot_dim (default all) of
+    head_dim values; layout "interleaved" / "half"; axes None (one position
+    per row) or three axis widths; scaling "plain", "linear", "base", "ramp"
+    or "band" (include/qi21.h gives the frequencies)."""
+    r = Rope()
+    if layout not in ROPE_LAYOUTS:
+        raise ValueError(f"layout {layout!r} (one of {sorted(ROPE_LAYOUTS)})")
+    if scaling not in ROPE_SCALINGS:
+        raise ValueError(f"scaling {scaling!r} (one of {sorted(ROPE_SCALINGS)})")
+    if axes is not None and len(axes) != 3:
+        raise ValueError("axes must be three widths")
+    check(load().qi21_rope_init(C.byref(r), head_dim, head_dim if rot_dim is None else rot_dim, ROPE_LAYOUTS[layout],
+                                None if axes is None else (_i32 * 3)(*axes), base, ROPE_SCALINGS[scaling], factor,
+                                orig_len, fast_turns, slow_turns, out_scale))
+    return r
 
 
 def segs_array(segs):

@@ -202,6 +202,42 @@ cudaError_t make_attn_plan(const AttnArgs& a, AttnPlan* p);
 cudaError_t launch_attn_plan(const AttnPlan& p, cudaStream_t s);
 cudaError_t launch_attention(const AttnArgs& a, cudaStream_t s);
 
+// ------------------------------------------------------ paged K/V cache --
+
+// A rotation as the kernels take it (qi21_rope).
+constexpr int kRopePairs = 128;
+struct RopeDev {
+  int rot, naxes;
+  float scale;
+  uint8_t axis[kRopePairs];
+  uint64_t turns[kRopePairs];
+};
+
+// A batch over a paged cache as the kernels take it (qi21_paged, checked).
+struct PagedArgs {
+  void* pool;
+  int dt, npages, page_rows, kv_heads, dim, nseq;
+  const int32_t* table;
+  int table_stride;
+  int table_rows;  // table_stride * page_rows, at most 2^30
+  const int32_t* lens;
+  const int32_t* cu;
+  const int32_t* prefix_pages;
+  int prefix_len;
+};
+
+// Rotation of rows (layout half or interleaved), and the append of rows to
+// the paged cache (rot == 0: keys as they are; pos null: prefix + own row).
+cudaError_t launch_rope(const RopeDev& r, bool half, int elem, int rows, int heads, int dim, const void* x,
+                        int64_t ldx, void* out, int64_t ldo, const int64_t* pos, bool grad, cudaStream_t s);
+cudaError_t launch_kv_append(const PagedArgs& p, const RopeDev& r, bool half, int rows, const void* k,
+                             int64_t ldk, const void* v, int64_t ldv, const int64_t* pos, cudaStream_t s);
+
+// Attention over the paged cache: workspace bytes, and the launches.
+size_t attn_paged_bytes(const PagedArgs& p, int rows, int heads);
+cudaError_t launch_attn_paged(const PagedArgs& p, int rows, int heads, const void* q, int64_t ldq, void* out,
+                              int64_t ldo, bool causal, const uint32_t* vis, float scale, void* ws, cudaStream_t s);
+
 // --------------------------------------------------------------- device ----
 
 int sm_count();
@@ -218,6 +254,8 @@ bool profiling_on();
 unsigned int gemm_status_read_clear();
 unsigned int attn_status_read_clear();
 unsigned int probe_status_read_clear();
+unsigned int rope_status_read_clear();
+unsigned int paged_status_read_clear();
 cudaError_t launch_wait_probe(cudaStream_t s);
 unsigned int read_and_clear_status();
 

@@ -452,8 +452,9 @@ int qi21_graph_step_batch_fp8(const qi21_geom* g, const qi21_layer_fp8* layers,
                               float* x_out, const float* mods, void* workspace, size_t ws_bytes,
                               qi21_graph** out);
 
-/* Reads and clears the device status word (0 = fine; nonzero = a kernel
- * gave up waiting). Synchronises the device. */
+/* Reads and clears the device status word (0 = fine; bit 0 = a kernel gave
+ * up waiting, bit 1 = a paged call met a page or row outside its cache).
+ * Synchronises the device. */
 int qi21_device_status(void);
 
 /* Self-test of the kernels' bounded waits: enqueues on `stream` one CTA
@@ -579,6 +580,139 @@ int qi21_op_kvcopy(int32_t rows, int32_t dim, const void* panel, void* kv, void*
 int qi21_op_attention(int32_t dtype, int32_t nq, int32_t heads, const void* panel,
                       const void* kv_pre, int32_t n_pre, int32_t n_own, const uint32_t* vis,
                       void* out, void* stream);
+
+/* --------------------------------------------------- paged K/V cache ---- */
+/* A K/V cache in pages that the sequences of a batch take from one pool, a
+ * prefix that all of them share held once, with the rotation, the append
+ * and the attention that serve it (this library's addition: the pages keep
+ * one contiguous cache per prompt). The types, the row layout (K, then V)
+ * and the conventions are those of the entry points above; grouped heads
+ * (heads a multiple of kv_heads) and head widths 64 and 128 are taken.
+ * Nothing here allocates or synchronises; every call may be captured into a
+ * CUDA graph (descriptors are copied at the call, the device arrays they
+ * point to are read when the work runs, so their contents may change
+ * between replays). */
+
+/* Layouts of a rotation: pair j is (2j, 2j + 1) or (j, j + rot_dim / 2). */
+#define QI21_ROPE_INTERLEAVED 0
+#define QI21_ROPE_HALF 1
+/* Frequency rules (f_j = base^(-2j/d), d the width of the pair's axis):
+ *   PLAIN   f_j
+ *   LINEAR  f_j / factor
+ *   BASE    f_j with base * factor^(d / (d - 2)): the fastest pair keeps
+ *           its speed, the slowest is slowed by the factor
+ *   RAMP    f_j (1 - r) + f_j r / factor, r = clamp((j - lo) / (hi - lo), 0, 1),
+ *           lo = max(0, floor(p(fast_turns))), hi = min(d - 1, ceil(p(slow_turns))),
+ *           p(n) = d ln(orig_len / (2 pi n)) / (2 ln base), the pair that
+ *           turns n times over orig_len positions (hi - lo at least 1e-3)
+ *   BAND    f_j r + f_j (1 - r) / factor, r = clamp((n - slow_turns) /
+ *           (fast_turns - slow_turns), 0, 1), n = orig_len f_j / (2 pi) */
+#define QI21_ROPE_PLAIN 0
+#define QI21_ROPE_LINEAR 1
+#define QI21_ROPE_BASE 2
+#define QI21_ROPE_RAMP 3
+#define QI21_ROPE_BAND 4
+#define QI21_ROPE_MAX_PAIRS 128
+
+/* A rotation, filled by qi21_rope_init (plain data: copy it freely). Pair j
+ * of a vector at position p (int64, column axis[j] of the row's positions)
+ * turns by p * turns[j] / 2^64 of a full turn, modulo whole turns: the
+ * product modulo 2^64 reduces the angle exactly at every position (turns[j]
+ * itself is f_j / 2 pi to f64 precision, so the angle is off by at most
+ * |p| f_j 2^-51). */
+typedef struct qi21_rope {
+  int32_t head_dim; /* width of a head vector, even, <= 256 */
+  int32_t rot_dim;  /* leading values that turn, even, <= head_dim */
+  int32_t layout;   /* QI21_ROPE_INTERLEAVED or _HALF */
+  int32_t naxes;    /* positions per row: 1, or 3 (frame, h, w) */
+  float out_scale;  /* factor of the turned values */
+  uint8_t axis[QI21_ROPE_MAX_PAIRS];
+  uint64_t turns[QI21_ROPE_MAX_PAIRS];
+} qi21_rope;
+
+/* Fills *r on the host. axes: NULL for one position per row, else the three
+ * axis widths (even, summing to rot_dim; pairs in axis order, as
+ * qi21_geom::axes). kind: a frequency rule; factor >= 1 (finite); orig_len,
+ * fast_turns > slow_turns > 0 are read by RAMP and BAND only (an fast_turns
+ * and slow_turns of 0 stand for 32 and 1 in RAMP, 4 and 1 in BAND).
+ * out_scale: 0 stands for 0.1 ln(factor) + 1 in RAMP and 1 otherwise.
+ * base > 1. */
+int qi21_rope_init(qi21_rope* r, int32_t head_dim, int32_t rot_dim, int32_t layout, const int32_t* axes,
+                   double base, int32_t kind, double factor, double orig_len, double fast_turns,
+                   double slow_turns, double out_scale);
+
+/* out[t][h] = x[t][h] turned by the row's positions (grad == 0), or the
+ * gradient of that with respect to x, given x as the gradient of its result
+ * (grad == 1: turned back, same out_scale). elem_type QI21_ELEM_F16, _BF16
+ * or _F32, of x and out; f32 arithmetic, one rounding. x [rows][heads]
+ * [head_dim] with ldx elements from row to row (ldx >= heads * head_dim, so
+ * q and k can be read out of a q|k|v panel), out likewise with ldo. out may
+ * be x itself with ldo == ldx (in place; columns past rot_dim are then left
+ * alone) and must not overlap x otherwise. pos device int64 [rows][naxes].
+ * Any alignment of the element; 16-byte aligned rows are fastest. */
+int qi21_op_rope(const qi21_rope* r, int32_t elem_type, int32_t rows, int32_t heads, const void* x,
+                 int64_t ldx, void* out, int64_t ldo, const int64_t* pos, int32_t grad, void* stream);
+
+/* A batch over a paged cache. A page holds page_rows rows [2][kv_heads]
+ * [head_dim] of the 16-bit dtype, K then V: the row layout [2H] of
+ * qi21_kvcache. Own row i of sequence b is row i % page_rows of page
+ * table[b][i / page_rows]; the prefix, prefix_len rows long, fills the pages
+ * prefix_pages in order and comes before every sequence's own rows. Row t of
+ * a call's rows (new keys, or queries) belongs to the sequence b with
+ * cu[b] <= t < cu[b + 1] and is the sequence's own row
+ * lens[b] - (cu[b + 1] - cu[b]) + (t - cu[b]): the call's rows are the
+ * sequence's last. Rows from cu[nseq] on are padding: not read, and their
+ * outputs are left as they were. Device arrays are read when the work runs.
+ * A page id outside [0, npages), where a row needs one, a negative own row
+ * or one past the table raises bit 1 (value 2) of the device status word:
+ * an append skips the row, the attention takes the page's keys and values
+ * as zeros. Entries that no row needs are not looked at. */
+typedef struct qi21_paged {
+  void* pool;                  /* dtype [npages][page_rows][2][kv_heads][head_dim], 16-byte aligned */
+  int32_t dtype;               /* QI21_DTYPE_F16 or _BF16 */
+  int32_t npages;
+  int32_t page_rows;           /* a multiple of 16 */
+  int32_t kv_heads;
+  int32_t head_dim;            /* 64 or 128 */
+  int32_t nseq;
+  const int32_t* table;        /* device [nseq][table_stride] */
+  int32_t table_stride;        /* pages per sequence at most */
+  const int32_t* lens;         /* device [nseq] own rows, the call's among them */
+  const int32_t* cu;           /* device [nseq + 1] first row of each sequence, non-decreasing from 0 */
+  const int32_t* prefix_pages; /* device [ceil(prefix_len / page_rows)], NULL if prefix_len == 0 */
+  int32_t prefix_len;
+} qi21_paged;
+
+/* Writes the call's `rows` new keys and values (k, v: dtype [rows][kv_heads]
+ * [head_dim], ldk / ldv elements from row to row) to their places in the
+ * cache, the keys turned on the way by *rope (NULL: as they are). pos device
+ * int64 [rows][naxes], or NULL with one position per row: prefix_len + own
+ * row. Two rows of a call must not have the same place (which one is kept,
+ * or a mix of both, is not defined). k and v must not lie in the pool. */
+int qi21_op_kv_append(const qi21_paged* kv, int32_t rows, const void* k, int64_t ldk, const void* v,
+                      int64_t ldv, const qi21_rope* rope, const int64_t* pos, void* stream);
+
+/* Workspace bytes of qi21_op_attention_paged for up to `rows` query rows of
+ * `heads` heads (0 on a bad descriptor; see qi21_last_error). */
+size_t qi21_attention_paged_bytes(const qi21_paged* kv, int32_t rows, int32_t heads);
+
+/* Attention of the call's query rows over [prefix, own rows] of their
+ * sequences: out = softmax(scale q k^T) v, the query heads [h g, (h + 1) g)
+ * sharing key head h (g = heads / kv_heads). Query row t sees a leading run
+ * of its keys: all of them, with causal != 0 those up to its own row, with
+ * vis (device uint32 [rows], takes the place of causal) the first
+ * min(vis[t], keys). A row that sees no key is 0. q dtype [rows][heads]
+ * [head_dim] with ldq elements from row to row, out likewise with ldo (must
+ * not overlap q); both 16-byte aligned, ldq and ldo multiples of 8. scale
+ * > 0 and finite. f32 scores, softmax and sums. When the rows of a sequence
+ * are few the prefix's part is computed once for the rows of all sequences;
+ * parts meet in the workspace (device, 256-byte aligned, at least
+ * qi21_attention_paged_bytes; needs no initial value; calls, or graphs, that
+ * share one must not overlap in time). Values behind a sequence's end, in
+ * the last page, are not used, whatever they are. */
+int qi21_op_attention_paged(const qi21_paged* kv, int32_t rows, int32_t heads, const void* q, int64_t ldq,
+                            void* out, int64_t ldo, int32_t causal, const uint32_t* vis, float scale,
+                            void* workspace, size_t ws_bytes, void* stream);
 
 #ifdef __cplusplus
 }
