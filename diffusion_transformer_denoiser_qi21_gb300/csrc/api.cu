@@ -67,7 +67,7 @@ int sm_count() {
 unsigned int read_and_clear_status() {
   cudaDeviceSynchronize();
   return gemm_status_read_clear() | attn_status_read_clear() | probe_status_read_clear() | rope_status_read_clear() |
-         paged_status_read_clear();
+         paged_status_read_clear() | wide_status_read_clear();
 }
 
 // ---------------------------------------------------------- profiling ----

@@ -224,6 +224,8 @@ static int check_heads(const qi21_paged* kv, int32_t rows, int32_t heads) {
   if (rows < 0 || rows > (1 << 24)) return refuse(QI21_ERR_SHAPE, "rows %d (at most 2^24)", rows);
   if (heads < 1 || heads > 1024 || heads % kv->kv_heads)
     return refuse(QI21_ERR_SHAPE, "heads %d (a multiple of kv_heads %d, at most 1024)", heads, kv->kv_heads);
+  if (static_cast<int64_t>(rows) * heads > (1 << 30))
+    return refuse(QI21_ERR_SHAPE, "rows * heads above 2^30 (%d * %d)", rows, heads);
   return QI21_OK;
 }
 

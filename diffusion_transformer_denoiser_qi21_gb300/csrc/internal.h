@@ -197,6 +197,11 @@ struct AttnPlan {
   int gx, gy, gz;  // grid; gx == 0: nothing to launch
 };
 
+// Tensor map of a 16-bit tensor (rank 2 or 3, dims innermost first, strides
+// in bytes of the outer dims) for boxes of 64 columns, 128-byte swizzle.
+cudaError_t encode_map(CUtensorMap* m, int dt, int rank, const void* ptr, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box);
+
 // Encode the maps of an attention launch (launches nothing), then launch.
 cudaError_t make_attn_plan(const AttnArgs& a, AttnPlan* p);
 cudaError_t launch_attn_plan(const AttnPlan& p, cudaStream_t s);
@@ -256,6 +261,7 @@ unsigned int attn_status_read_clear();
 unsigned int probe_status_read_clear();
 unsigned int rope_status_read_clear();
 unsigned int paged_status_read_clear();
+unsigned int wide_status_read_clear();
 cudaError_t launch_wait_probe(cudaStream_t s);
 unsigned int read_and_clear_status();
 

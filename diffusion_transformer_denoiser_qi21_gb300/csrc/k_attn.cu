@@ -49,6 +49,7 @@
 
 #include <cudaTypedefs.h>
 
+#include "attn.cuh"
 #include "internal.h"
 #include "ptx.cuh"
 
@@ -83,89 +84,6 @@ constexpr int kAttnSmem = kOffBar + 512 + 1024;
 constexpr int kAttnThreads = 352;           // 11 warps
 constexpr float kRescaleThreshold = 8.0f;  // log2 units: P <= 2^8 in f16
 static_assert(kNBar * 8 + 8 <= 512, "barrier area");
-
-__device__ __forceinline__ float ex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
-
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
-}
-
-__device__ __forceinline__ uint64_t f2(float lo, float hi) {
-  uint64_t r;
-  asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(lo), "f"(hi));
-  return r;
-}
-
-__device__ __forceinline__ void unf2(uint64_t v, float& lo, float& hi) {
-  asm("mov.b64 {%0, %1}, %2;" : "=f"(lo), "=f"(hi) : "l"(v));
-}
-
-__device__ __forceinline__ uint64_t ffma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-
-__device__ __forceinline__ uint64_t fadd2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// Pair form of the A-from-TMEM MMA: each CTA of the pair supplies its 128
-// lanes of A (same TMEM address) and half of B's N columns.
-__device__ __forceinline__ void tc_mma_f16_ts_pair(uint32_t d_tmem, uint32_t a_tmem, uint64_t b_desc,
-                                                   uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::2.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(b_desc), "r"(idesc), "r"(accumulate)
-      : "memory");
-}
-
-// Arrive on an mbarrier of the cluster without memory ordering: the data it
-// announces (TMEM stores) were completed by tcgen05.wait::st and ordered
-// by tcgen05.fence::before_thread_sync.
-__device__ __forceinline__ void mbar_arrive_cluster_relaxed(uint32_t bar_cluster) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar_cluster) : "memory");
-}
-
-#define QI21_A8(i) "=r"(r[i]), "=r"(r[i + 1]), "=r"(r[i + 2]), "=r"(r[i + 3]), \
-                   "=r"(r[i + 4]), "=r"(r[i + 5]), "=r"(r[i + 6]), "=r"(r[i + 7])
-#define QI21_I8(i) "r"(r[i]), "r"(r[i + 1]), "r"(r[i + 2]), "r"(r[i + 3]), \
-                   "r"(r[i + 4]), "r"(r[i + 5]), "r"(r[i + 6]), "r"(r[i + 7])
-#define QI21_REGS32 "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, " \
-                    "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}"
-#define QI21_REGS32_1 "{%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, %16, " \
-                      "%17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31, %32}"
-
-// 16 TMEM lanes from the lane in taddr, 8 repetitions of 8 columns: thread t
-// gets rows (t/4, t/4 + 8) x columns (2 (t%4), +1) of each repetition,
-// in the order (row, col), (row, col + 1), (row + 8, col), (row + 8, col + 1).
-__device__ __forceinline__ void tmem_ld16x256_x8(uint32_t taddr, uint32_t (&r)[32]) {
-  asm volatile("tcgen05.ld.sync.aligned.16x256b.x8.b32 " QI21_REGS32 ", [%32];"
-               : QI21_A8(0), QI21_A8(8), QI21_A8(16), QI21_A8(24)
-               : "r"(taddr));
-}
-__device__ __forceinline__ void tmem_st16x256_x8(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile("tcgen05.st.sync.aligned.16x256b.x8.b32 [%0], " QI21_REGS32_1 ";" ::"r"(taddr), QI21_I8(0),
-               QI21_I8(8), QI21_I8(16), QI21_I8(24)
-               : "memory");
-}
-// 16 TMEM lanes, 16 repetitions of 4 columns: thread t writes rows (t/4,
-// t/4 + 8) of column t%4 of each repetition, row t/4 first.
-__device__ __forceinline__ void tmem_st16x128_x16(uint32_t taddr, const uint32_t (&r)[32]) {
-  asm volatile("tcgen05.st.sync.aligned.16x128b.x16.b32 [%0], " QI21_REGS32_1 ";" ::"r"(taddr), QI21_I8(0),
-               QI21_I8(8), QI21_I8(16), QI21_I8(24)
-               : "memory");
-}
 
 // key index of virtual key v (cache keys, padding, then own keys), or a
 // value no limit reaches for a padding key
@@ -530,23 +448,34 @@ static PFN_cuTensorMapEncodeTiled_v12000 attn_encode_fn() {
   return fn;
 }
 
-static cudaError_t encode_rows(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint32_t box_rows,
-                               int dt) {
+cudaError_t encode_map(CUtensorMap* m, int dt, int rank, const void* ptr, const uint64_t* dims, const uint64_t* strides,
+                       const uint32_t* box) {
   auto fn = attn_encode_fn();
   if (fn == nullptr) return cudaErrorNotSupported;
-  cuuint64_t dims[2] = {cols, rows};
-  cuuint64_t strides[1] = {cols * 2};
-  cuuint32_t box[2] = {64, box_rows};
-  cuuint32_t es[2] = {1, 1};
+  cuuint64_t d[3], st[2];
+  cuuint32_t bx[3], es[3];
+  for (int i = 0; i < rank; ++i) {
+    d[i] = dims[i];
+    bx[i] = box[i];
+    es[i] = 1;
+    if (i + 1 < rank) st[i] = strides[i];
+  }
   const CUtensorMapDataType type = dt == DT_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16;
   auto encode = [&] {
-    return fn(m, type, 2, const_cast<void*>(ptr), dims, strides, box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+    return fn(m, type, rank, const_cast<void*>(ptr), d, st, bx, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   };
   CUresult r = encode();
   // a host thread whose first library call this is may have no context yet
   if (r == CUDA_ERROR_INVALID_CONTEXT && bind_primary_context()) r = encode();
   return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+static cudaError_t encode_rows(CUtensorMap* m, const void* ptr, uint64_t cols, uint64_t rows, uint32_t box_rows,
+                               int dt) {
+  const uint64_t dims[2] = {cols, rows}, strides[1] = {cols * 2};
+  const uint32_t box[2] = {64, box_rows};
+  return encode_map(m, dt, 2, ptr, dims, strides, box);
 }
 
 cudaError_t make_attn_plan(const AttnArgs& in, AttnPlan* p) {

@@ -9,6 +9,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "attn.cuh"
 #include "internal.h"
 #include "paged.cuh"
 #include "ptx.cuh"
@@ -26,29 +27,6 @@ unsigned int paged_status_read_clear() {
 
 constexpr int kGran = 16;               // keys of a granule: never crosses a page
 constexpr int kWarps = 4;               // of a CTA
-constexpr float kPagedRescale = 8.0f;   // log2 units: p <= 2^8, in f16 range
-
-struct PagedAttnArgs {
-  PagedArgs kv;
-  const void* q;
-  void* out;
-  int64_t ldq, ldo;
-  int rows, heads, group;  // group: query heads of a key head
-  int causal;
-  const uint32_t* vis;
-  float scale_log2;
-  int pre_tiles, pre_splits;  // CTAs of the prefix: tiles x splits
-  int own_tiles, own_splits;
-  int slots;                  // parts per row; 1: the part is the result
-  float* part_o;              // [slots][rows][heads][dim]
-  float2* part_ml;            // [slots][rows][heads] (max in log2 units, sum)
-};
-
-__device__ __forceinline__ float pex2(float x) {
-  float y;
-  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-  return y;
-}
 
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
@@ -88,39 +66,6 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
         "{%0, %1, %2, %3};"
         : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
         : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-
-// New rows of sequence b: 0 for ends that do not fit the call's rows.
-__device__ __forceinline__ int seq_rows(const PagedAttnArgs& a, int b) {
-  const int c0 = __ldg(a.kv.cu + b), c1 = __ldg(a.kv.cu + b + 1);
-  return (c0 >= 0 && c1 <= a.rows && c1 > c0) ? c1 - c0 : 0;
-}
-
-// The x-th tile of `tile` (row, head) pairs, counted over the sequences in
-// order: its sequence and its place there, by one whole warp (32 sequences
-// per round). b == nseq: there are fewer tiles.
-__device__ __forceinline__ void warp_find_tile(const PagedAttnArgs& a, int x, int tile, int lane, int& b, int& at) {
-  int before = 0;
-  for (int b0 = 0; b0 < a.kv.nseq; b0 += 32) {
-    int n = 0;
-    if (b0 + lane < a.kv.nseq) n = (seq_rows(a, b0 + lane) * a.group + tile - 1) / tile;
-    int sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int up = __shfl_up_sync(0xffffffffu, sum, o);
-      if (lane >= o) sum += up;
-    }
-    const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
-    if (past) {
-      const int l = __ffs(past) - 1;
-      b = b0 + l;
-      at = x - before - __shfl_sync(0xffffffffu, sum - n, l);
-      return;
-    }
-    before += __shfl_sync(0xffffffffu, sum, 31);
-  }
-  b = a.kv.nseq;
-  at = 0;
 }
 
 // ------------------------------------------------------- few rows a tile --
@@ -170,7 +115,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     nsplit = a.own_splits;
     slot = a.pre_splits + split;
     int b, at;
-    warp_find_tile(a, tile, R, lane, b, at);
+    warp_find_tile(a, tile, a.group, R, lane, b, at);
     if (b >= a.kv.nseq) return;
     t0 = __ldg(a.kv.cu + b);
     nrows = seq_rows(a, b);
@@ -329,7 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
         // the maximum is raised only past the threshold: o and l share it
         al[e] = 1.f;
         if (mx > m[mt][e] + kPagedRescale) {
-          al[e] = pex2(m[mt][e] - mx);
+          al[e] = ex2(m[mt][e] - mx);
           m[mt][e] = mx;
           moved = true;
         }
@@ -337,7 +282,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
         float sum = 0.f;
 #pragma unroll
         for (int n = 0; n < 2; ++n) {
-          const float p0 = pex2(s[mt][n][2 * e] - base), p1 = pex2(s[mt][n][2 * e + 1] - base);
+          const float p0 = ex2(s[mt][n][2 * e] - base), p1 = ex2(s[mt][n][2 * e + 1] - base);
           sum += p0 + p1;
           // P is rounded to the values' type for the MMA (half a step of a
           // weight each, of either sign); l sums the f32 weights
@@ -408,7 +353,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) {
-      const float f = pex2(s_m[w][r] - base);
+      const float f = ex2(s_m[w][r] - base);
       const float4 v = *reinterpret_cast<const float4*>(
           reinterpret_cast<const float*>(smem + w * (NST * 2 * HALF)) + r * OP + c);
       ll += f * s_l[w][r];
@@ -454,13 +399,14 @@ __global__ void __launch_bounds__(256) attn_paged_join(const __grid_constant__ P
     float w = 0.f;
     if (s0 + lane < a.slots) {
       const float2 ml = a.part_ml[(s0 + lane) * step + pair];
-      w = pex2(ml.x - base);
+      w = ex2(ml.x - base);
       ll += w * ml.y;
     }
     const int n = min(32, a.slots - s0);
 #pragma unroll 4
     for (int s = 0; s < n; ++s) {
       const float ws = __shfl_sync(0xffffffffu, w, s);
+      if (ws == 0.f) continue;  // a part without keys may hold no sums
       const float* src = a.part_o + ((s0 + s) * step + pair) * D + lane * V;
       if (V == 4) {
         const float4 v = *reinterpret_cast<const float4*>(src);
@@ -500,6 +446,24 @@ size_t attn_paged_bytes(const PagedArgs& p, int rows, int heads) {
   return most * heads * (static_cast<size_t>(p.dim) * 4 + 8) + 256;
 }
 
+// Parts of a wide call's keys: the count that ends first, by a model of one
+// item's time in key blocks (its blocks, and about four of set-up and end)
+// over the waves of items, plus the parts' write and read back at about
+// 6 TB/s against 0.8 us a block.
+static int wide_splits(int64_t items, int64_t blocks, int64_t slots, int64_t rows_heads, int dim, int most) {
+  int best = 1;
+  double least = 0.0;
+  for (int n = 1; n <= most && n <= blocks; ++n) {
+    const double t = static_cast<double>((items * n + slots - 1) / slots) * ((blocks + n - 1) / n + 4) +
+                     (n > 1 ? n * static_cast<double>(rows_heads) * dim * 8 / 4.8e6 : 0.0);
+    if (n == 1 || t < least) {
+      best = n;
+      least = t;
+    }
+  }
+  return best;
+}
+
 template <bool BF, int D>
 static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   constexpr int smem = kNarrowSmem<D>;
@@ -509,30 +473,63 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   });
   if (attr == nullptr) return cudaErrorNoDevice;
   if (*attr != cudaSuccess) return *attr;
-  const int64_t pairs = static_cast<int64_t>(a.rows) * a.group;
-  const int hk = a.kv.kv_heads;
-  const int R = 16;
-  a.own_tiles = static_cast<int>(pairs / R + std::min<int64_t>(a.kv.nseq, a.rows));
-  a.pre_tiles = a.kv.prefix_len > 0 ? static_cast<int>((pairs + R - 1) / R) : 0;
-  // splits: enough CTAs for two waves of two per SM, none of fewer than 256 keys
-  const int64_t want = 4 * static_cast<int64_t>(sm_count());
+  const int hk = a.kv.kv_heads, P = a.kv.prefix_len;
+  const int64_t pairs = static_cast<int64_t>(a.rows) * a.group, all = static_cast<int64_t>(a.rows) * a.heads;
+  const int seqs = std::min(a.kv.nseq, a.rows);
   const int most = paged_slots(a.rows);
+  const int tokens = a.kv.npages > 0 ? wide_tokens(a.group) : 0;
+  cudaError_t e = cudaSuccess;
+  auto join = [&] {
+    attn_paged_join<BF, D><<<static_cast<unsigned>((all + 7) / 8), 256, 0, s>>>(a);
+    return cudaGetLastError();
+  };
+  auto place_parts = [&] {
+    a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.slots) * a.rows * a.heads * D);
+  };
+  if (tokens > 0 && pairs >= 64 * static_cast<int64_t>(seqs)) {
+    // many rows per sequence: a sequence's tiles walk [prefix, own keys]
+    const bool pair = D == 128 && pairs > 128 * static_cast<int64_t>(seqs);
+    const int per = tokens * (pair ? 2 : 1);
+    const int64_t tiles = a.rows / per + seqs;
+    const int64_t blocks = (static_cast<int64_t>(P) + 127) / 128 + (static_cast<int64_t>(a.kv.table_rows) + 127) / 128;
+    if (tiles > 0x3fffffff / kMaxSlots) return cudaErrorInvalidValue;
+    a.slots = wide_splits(tiles * hk, blocks, sm_count() / (pair ? 2 : 1), all, D, most);
+    place_parts();
+    e = launch_attn_wide(a, WIDE_JOINT, pair, static_cast<int>(tiles), a.slots, s);
+    return e != cudaSuccess || a.slots == 1 ? e : join();
+  }
+  // few rows per sequence: the prefix for the rows of all sequences, each
+  // sequence's own keys for its own
+  const int R = 16;
+  a.own_tiles = static_cast<int>(pairs / R + seqs);
+  // narrow splits: enough CTAs for two waves of two per SM, none of fewer
+  // than 256 keys
+  const int64_t want = 4 * static_cast<int64_t>(sm_count());
   auto splits = [&](int64_t tiles, int64_t keys, int cap) {
     const int64_t n = std::min<int64_t>((want + tiles * hk - 1) / (tiles * hk), (keys + 255) / 256);
     return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, cap)));
   };
-  a.pre_splits = a.pre_tiles ? splits(a.pre_tiles, a.kv.prefix_len, most - 1) : 0;
+  const bool wide = P > 0 && tokens > 0 && pairs > R;
+  const bool pair = D == 128 && pairs > 128;
+  const int per = tokens * (pair ? 2 : 1);
+  int wide_tiles = 0;
+  if (wide) {
+    wide_tiles = (a.rows + per - 1) / per;
+    a.pre_splits = wide_splits(static_cast<int64_t>(wide_tiles) * hk, (static_cast<int64_t>(P) + 127) / 128,
+                               sm_count() / (pair ? 2 : 1), all, D, most - 1);
+  } else if (P > 0) {
+    a.pre_tiles = static_cast<int>((pairs + R - 1) / R);
+    a.pre_splits = splits(a.pre_tiles, P, most - 1);
+  }
   a.own_splits = splits(a.own_tiles, a.kv.table_rows, most - a.pre_splits);
   a.slots = a.pre_splits + a.own_splits;
-  a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.slots) * a.rows * a.heads * D);
+  place_parts();
+  if (wide && (e = launch_attn_wide(a, WIDE_PREFIX, pair, wide_tiles, a.pre_splits, s)) != cudaSuccess) return e;
   const int64_t gx = static_cast<int64_t>(a.pre_tiles) * a.pre_splits + static_cast<int64_t>(a.own_tiles) * a.own_splits;
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   attn_paged_narrow<BF, D, 1><<<dim3(static_cast<unsigned>(gx), hk), kWarps * 32, smem, s>>>(a);
-  cudaError_t e = cudaGetLastError();
-  if (e != cudaSuccess || a.slots == 1) return e;
-  const int64_t all = static_cast<int64_t>(a.rows) * a.heads;
-  attn_paged_join<BF, D><<<static_cast<unsigned>((all + 7) / 8), 256, 0, s>>>(a);
-  return cudaGetLastError();
+  e = cudaGetLastError();
+  return e != cudaSuccess || a.slots == 1 ? e : join();
 }
 
 cudaError_t launch_attn_paged(const PagedArgs& p, int rows, int heads, const void* q, int64_t ldq, void* out,

@@ -42,4 +42,63 @@ __device__ __forceinline__ int64_t paged_row(const PagedArgs& p, int b, int own,
   return -1;
 }
 
+constexpr float kPagedRescale = 8.0f;  // log2 units: p <= 2^8, in f16 range
+
+// One attention call over a paged cache.
+struct PagedAttnArgs {
+  PagedArgs kv;
+  const void* q;
+  void* out;
+  int64_t ldq, ldo;
+  int rows, heads, group;  // group: query heads of a key head
+  int causal;
+  const uint32_t* vis;
+  float scale_log2;
+  int pre_tiles, pre_splits;  // CTAs of the prefix: tiles x splits
+  int own_tiles, own_splits;
+  int slots;                  // parts per row; 1: the part is the result
+  float* part_o;              // [slots][rows][heads][dim]
+  float2* part_ml;            // [slots][rows][heads] (max in log2 units, sum)
+};
+
+// New rows of sequence b: 0 for ends that do not fit the call's rows.
+__device__ __forceinline__ int seq_rows(const PagedAttnArgs& a, int b) {
+  const int c0 = __ldg(a.kv.cu + b), c1 = __ldg(a.kv.cu + b + 1);
+  return (c0 >= 0 && c1 <= a.rows && c1 > c0) ? c1 - c0 : 0;
+}
+
+// The x-th tile, counted over the sequences in order, of `tile` of the `per`
+// pieces that a row has: its sequence and its place there, by one whole
+// warp (32 sequences per round). b == nseq: there are fewer tiles.
+__device__ __forceinline__ void warp_find_tile(const PagedAttnArgs& a, int x, int per, int tile, int lane, int& b,
+                                               int& at) {
+  int before = 0;
+  for (int b0 = 0; b0 < a.kv.nseq; b0 += 32) {
+    int n = 0;
+    if (b0 + lane < a.kv.nseq) n = (seq_rows(a, b0 + lane) * per + tile - 1) / tile;
+    int sum = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int up = __shfl_up_sync(0xffffffffu, sum, o);
+      if (lane >= o) sum += up;
+    }
+    const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
+    if (past) {
+      const int l = __ffs(past) - 1;
+      b = b0 + l;
+      at = x - before - __shfl_sync(0xffffffffu, sum - n, l);
+      return;
+    }
+    before += __shfl_sync(0xffffffffu, sum, 31);
+  }
+  b = a.kv.nseq;
+  at = 0;
+}
+
+// Tiles of many rows on the tensor cores (k_paged_tc.cu).
+enum WideMode : int { WIDE_PREFIX = 0, WIDE_JOINT = 1 };
+// Tokens of a CTA's tile, 0 if the group does not fit one.
+inline int wide_tokens(int group) { return group <= 128 ? 128 / group : 0; }
+cudaError_t launch_attn_wide(const PagedAttnArgs& a, WideMode mode, bool pair, int tiles, int splits, cudaStream_t s);
+
 }  // namespace qi21
