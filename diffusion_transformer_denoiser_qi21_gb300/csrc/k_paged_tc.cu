@@ -6,14 +6,15 @@
 // they are the rows of all sequences and walk the prefix (WIDE_PREFIX); its
 // key blocks may be split over CTAs, whose parts are joined later.
 //
-// 11 warps, as in the attention over one contiguous prefix:
-//   warp 0     TMA: Q, then 128-key blocks of K and V into rings, each as
+// 12 warps, as in the attention over one contiguous prefix, with a second
+// loading warp:
+//   warps 0,11 TMA: Q and 128-key blocks of K, and of V, into rings, each as
 //              boxes of neighbouring rows of one page (as many as the page
-//              size and 64 allow), a lane per box. Boxes behind the end are
-//              zeros. The rows of a V box behind the end within a page are
-//              whatever the page held (0 times a NaN is a NaN, so a weight
-//              of 0 does not take them out): that one box is copied by the
-//              warp with zeros in their place.
+//              size and 64 allow). Boxes behind the end are zeros. The rows
+//              of a V box behind the end within a page are whatever the page
+//              held (0 times a NaN is a NaN, so a weight of 0 does not take
+//              them out): that one box is copied by the warp with zeros in
+//              their place.
 //   warp 1     S_j = Q K_j^T into one of three TMEM buffers
 //   warp 10    O += P_j V_j, P read from TMEM
 //   warps 2-9  softmax, 16 TMEM lanes (rows) each
@@ -44,8 +45,8 @@ unsigned int wide_status_read_clear() {
 }
 
 constexpr int kWK = 128;                 // keys per block
-constexpr int kWBox = 64;                // rows per K / V box at most
-constexpr int kWThreads = 352;
+constexpr int kWBoxShift = 6;            // log2 of the rows per K / V box at most
+constexpr int kWThreads = 384;            // 12 warps
 constexpr int kWNS = 3;                  // S / P buffers in TMEM
 
 template <int D, bool PAIR>
@@ -70,7 +71,7 @@ struct WideArgs {
   CUtensorMap qmap;   // q [rows][heads][dim], box tokens x group x 64 columns
   CUtensorMap kvmap;  // pool [npages * page_rows][2 * kv_heads * dim], box br x 64
   int tokens;         // of a CTA's tile
-  int br;             // rows of a K / V box
+  int br_shift;       // log2 of the rows of a K / V box
   int joint, splits, tiles;
 };
 
@@ -200,7 +201,7 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
   auto cut = [&](int j) {
     const bool pre = j < npb;
     const int left = (pre ? np : no) - (pre ? j : j - npb) * kWK;
-    return left < kWK && left % p.br != 0;
+    return left < kWK && (left & ((1 << p.br_shift) - 1)) != 0;
   };
 
   // a wait by a whole warp: every lane leaves with the same answer
@@ -208,9 +209,14 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
     return __all_sync(0xffffffffu, mbar_wait(bar, parity, abort_flag, &s_wide_status));
   };
 
-  if (warp == 0) {
+  if (warp == 0 || warp == 11) {
+    // the two loading warps: Q and the K blocks, and the V blocks. A lane
+    // holds the pool row of one box of a run of blocks, the ids of the next
+    // run's pages are under way meanwhile, and lane 0 issues the boxes: a
+    // block must not wait for its page ids, nor K for V's stage
     if (n > 0) {
-      if (lane == 0) {
+      const bool is_k = warp == 0;
+      if (is_k && lane == 0) {
         const uint32_t bytes = static_cast<uint32_t>(W::kCols) * p.tokens * a.group * 128;
         if (leader) mbar_arrive_expect_tx(qfull, CT * bytes);
         for (int c = 0; c < W::kCols; ++c) {
@@ -220,70 +226,81 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
             tma_load_3d(smem + c * 16384, &p.qmap, qfull, c * 64, hk * a.group, tok0);
         }
       }
-      const int nkb = W::kKeysK / p.br;  // boxes of K per column piece
-      const int nvb = kWK / p.br;        // boxes of V per column piece
-      const int none = a.kv.npages * a.kv.page_rows;  // a row behind the pool: zeros
-      // pool row of `key` of block j's source, or `none`
-      auto row_of = [&](bool pre, int key, int end) {
-        if (key >= end) return none;
-        const int32_t* pages = pre ? a.kv.prefix_pages : own_pages;
-        const int pg = key / a.kv.page_rows;
-        const int id = __ldg(pages + pg);
+      const int brs = p.br_shift;
+      const int keys = is_k ? W::kKeysK : kWK;              // of a block, in this CTA
+      const int boxes = keys >> brs;                        // per column piece: 1, 2, 4 or 8
+      const int bxs = (is_k && PAIR ? 6 : 7) - brs;         // log2
+      const int run = 32 >> bxs;                            // blocks of a run
+      const int koff = (is_k ? rank * W::kKeysK : 0) + ((lane & (boxes - 1)) << brs);
+      const int none = a.kv.npages * a.kv.page_rows;        // a row behind the pool: zeros
+      // this lane's box of the run from block i on: its key (-1: behind the
+      // end) and its page id
+      int key, id;
+      auto ids = [&](int i) {
+        const int j = j0 + i + (lane >> bxs);
+        const bool pre = j < npb;
+        key = (pre ? j : j - npb) * kWK + koff;
+        if (i + (lane >> bxs) >= n || key >= (pre ? np : no)) key = -1;
+        if (key >= 0) id = __ldg((pre ? a.kv.prefix_pages : own_pages) + key / a.kv.page_rows);
+      };
+      auto row_of = [&]() {
+        if (key < 0) return none;
         if (id < 0 || id >= a.kv.npages) {
           atomicOr(&s_wide_status, kStatusPage);
           return none;
         }
-        return id * a.kv.page_rows + (key - pg * a.kv.page_rows);
+        return id * a.kv.page_rows + key % a.kv.page_rows;
       };
-      auto k_row = [&](int j) {  // this lane's box of K of block j
-        const bool pre = j < npb;
-        const int key = (pre ? j : j - npb) * kWK + rank * W::kKeysK + (lane % nkb) * p.br;
-        return lane < nkb * W::kCols ? row_of(pre, key, pre ? np : no) : none;
-      };
-      auto v_row = [&](int j) {
-        const bool pre = j < npb;
-        const int key = (pre ? j : j - npb) * kWK + (lane % nvb) * p.br;
-        return lane < nvb * W::kColsV ? row_of(pre, key, pre ? np : no) : none;
-      };
-      auto load_k = [&](int i, int row) -> bool {
-        const int st = i % NK;
-        if (!wait_all(&kempty[st], ((i / NK) & 1) ^ 1u)) return false;
-        if (lane == 0 && leader) mbar_arrive_expect_tx(&kfull[st], CT * W::kK);
-        __syncwarp();
-        if (lane < nkb * W::kCols) {
-          const int c = lane / nkb, b = lane % nkb;
-          uint8_t* d = smem + W::kOffK + st * W::kK + c * (W::kKeysK * 128) + b * p.br * 128;
-          const int col = hk * D + c * 64;
-          if (PAIR)
-            tma_load_2d_pair(d, &p.kvmap, mapa_rank(&kfull[st], 0), col, row);
-          else
-            tma_load_2d(d, &p.kvmap, &kfull[st], col, row);
+      uint64_t* full = is_k ? kfull : vfull;
+      uint64_t* empty = is_k ? kempty : vempty;
+      const int stage = is_k ? W::kK : W::kV;
+      const int cols = is_k ? W::kCols : W::kColsV;
+      const int piece = keys * 128;                         // bytes of a column piece
+      const int col0 = is_k ? hk * D : a.kv.kv_heads * D + hk * D + (PAIR ? rank * 64 : 0);
+      uint8_t* ring = smem + (is_k ? W::kOffK : W::kOffV);
+      bool ok = true;
+      int rows = none, tails = 0;
+      ids(0);
+      for (int i = 0; i < n && ok; ++i) {
+        if ((i & (run - 1)) == 0) {
+          rows = row_of();
+          ids(i + run);
         }
-        return true;
-      };
-      uint32_t tails = 0;
-      auto load_v = [&](int j, int i, int row) -> bool {
         const int st = i % NK;
-        if (!wait_all(&vempty[st], ((i / NK) & 1) ^ 1u)) return false;
-        uint8_t* base = smem + W::kOffV + st * W::kV;
-        const int col0 = a.kv.kv_heads * D + hk * D + (PAIR ? rank * 64 : 0);
-        int skip = -1;  // the cut box
-        if (cut(j)) {
+        if (!wait_all(&empty[st], ((i / NK) & 1) ^ 1u)) {
+          ok = false;
+          break;
+        }
+        uint8_t* base = ring + st * stage;
+        const int at = (i & (run - 1)) << bxs;  // the lane with the block's first box
+        int skip = -1;
+        if (!is_k && cut(j0 + i)) {
+          // the V box that the end cuts, rows behind it zero
+          const int j = j0 + i;
           const bool pre = j < npb;
-          const int end = pre ? np : no, key0 = (pre ? j : j - npb) * kWK;
-          skip = (end - key0) / p.br;
-          const int first = key0 + skip * p.br;
-          const int r0 = __shfl_sync(0xffffffffu, row, skip);  // lane `skip` has the box of column piece 0
-          for (int c = 0; c < W::kColsV; ++c) {
-            uint8_t* d = base + c * 16384 + skip * p.br * 128;
-            for (int u = lane; u < p.br * 8; u += 32) {
-              const int r = u >> 3, ch = u & 7;
-              uint4 v = make_uint4(0, 0, 0, 0);
-              if (first + r < end && r0 != none)
-                v = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.kv.pool) +
-                                                    (static_cast<int64_t>(r0) + r) * (2 * a.kv.kv_heads * D) + col0 +
-                                                    c * 64 + ch * 8);
-              *reinterpret_cast<uint4*>(d + r * 128 + ((ch ^ (r & 7)) << 4)) = v;
+          const int left = (pre ? np : no) - (pre ? j : j - npb) * kWK;
+          skip = left >> brs;
+          const int live = left - (skip << brs);  // its rows before the end
+          const int r0 = __shfl_sync(0xffffffffu, rows, at + skip);
+          const uint16_t* src = static_cast<const uint16_t*>(a.kv.pool) +
+                                static_cast<int64_t>(r0 == none ? 0 : r0) * (2 * a.kv.kv_heads * D) + col0;
+          for (int c = 0; c < cols; ++c) {
+            uint8_t* d = base + c * piece + (skip << (brs + 7));
+            for (int u0 = lane; u0 < 8 << brs; u0 += 128) {
+              uint4 v[4];
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = (u0 + 32 * k) >> 3, ch = u0 & 7;
+                v[k] = make_uint4(0, 0, 0, 0);
+                if (r < live && r0 != none)
+                  v[k] = *reinterpret_cast<const uint4*>(src + static_cast<int64_t>(r) * (2 * a.kv.kv_heads * D) +
+                                                         c * 64 + ch * 8);
+              }
+#pragma unroll
+              for (int k = 0; k < 4; ++k) {
+                const int r = (u0 + 32 * k) >> 3, ch = u0 & 7;
+                *reinterpret_cast<uint4*>(d + r * 128 + ((ch ^ (r & 7)) << 4)) = v[k];
+              }
             }
           }
           fence_proxy_async_smem();
@@ -292,37 +309,19 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
           ++tails;
         }
         if (lane == 0 && leader)
-          mbar_arrive_expect_tx(&vfull[st], CT * (W::kV - (skip >= 0 ? W::kColsV * p.br * 128 : 0)));
-        __syncwarp();
-        if (lane < nvb * W::kColsV && lane % nvb != skip) {
-          const int c = lane / nvb, b = lane % nvb;
-          uint8_t* d = base + c * 16384 + b * p.br * 128;
-          if (PAIR)
-            tma_load_2d_pair(d, &p.kvmap, mapa_rank(&vfull[st], 0), col0 + c * 64, row);
-          else
-            tma_load_2d(d, &p.kvmap, &vfull[st], col0 + c * 64, row);
-        }
-        return true;
-      };
-      // need order: K_0, K_1, then V_i before K_{i+2}; the page ids of a load
-      // are fetched one load ahead
-      bool ok = true;
-      int rk = k_row(j0);
-      for (int i = 0; i < min(2, n) && ok; ++i) {
-        const int r = rk;
-        if (i + 1 < n) rk = k_row(j0 + i + 1);
-        ok = load_k(i, r);
-      }
-      if (n > 2) rk = k_row(j0 + 2);
-      int rv = v_row(j0);
-      for (int i = 0; i < n && ok; ++i) {
-        const int r = rv;
-        if (i + 1 < n) rv = v_row(j0 + i + 1);
-        ok = load_v(j0 + i, i, r);
-        if (ok && i + 2 < n) {
-          const int r2 = rk;
-          if (i + 3 < n) rk = k_row(j0 + i + 3);
-          ok = load_k(i + 2, r2);
+          mbar_arrive_expect_tx(&full[st], CT * (stage - (skip >= 0 ? cols << (brs + 7) : 0)));
+        const uint32_t fb = PAIR ? mapa_rank(&full[st], 0) : 0u;
+        for (int b = 0; b < boxes; ++b) {
+          const int row = __shfl_sync(0xffffffffu, rows, at + b);
+          if (lane == 0 && b != skip) {
+            uint8_t* d = base + (b << (brs + 7));
+            for (int c = 0; c < cols; ++c) {
+              if (PAIR)
+                tma_load_2d_pair(d + c * piece, &p.kvmap, fb, col0 + c * 64, row);
+              else
+                tma_load_2d(d + c * piece, &p.kvmap, &full[st], col0 + c * 64, row);
+            }
+          }
         }
       }
       if (!ok) {
@@ -641,8 +640,8 @@ cudaError_t launch_attn_wide(const PagedAttnArgs& a, WideMode mode, bool pair, i
   memset(&w, 0, sizeof w);
   w.a = a;
   w.tokens = wide_tokens(a.group);
-  w.br = kWBox;
-  while (a.kv.page_rows % w.br) w.br /= 2;  // page_rows is a multiple of 16
+  w.br_shift = kWBoxShift;
+  while (a.kv.page_rows & ((1 << w.br_shift) - 1)) --w.br_shift;  // page_rows is a multiple of 16
   w.joint = mode == WIDE_JOINT;
   w.tiles = tiles;
   w.splits = splits;
@@ -655,7 +654,7 @@ cudaError_t launch_attn_wide(const PagedAttnArgs& a, WideMode mode, bool pair, i
   const uint64_t kd[2] = {2 * static_cast<uint64_t>(a.kv.kv_heads) * D,
                           static_cast<uint64_t>(a.kv.npages) * a.kv.page_rows};
   const uint64_t ks[1] = {kd[0] * 2};
-  const uint32_t kb[2] = {64, static_cast<uint32_t>(w.br)};
+  const uint32_t kb[2] = {64, 1u << w.br_shift};
   e = encode_map(&w.kvmap, a.kv.dt, 2, a.kv.pool, kd, ks, kb);
   if (e != cudaSuccess) return e;
   const bool bf = a.kv.dt == DT_BF16;
