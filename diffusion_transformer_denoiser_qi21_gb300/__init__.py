@@ -498,44 +498,65 @@ def op_attention(panel, heads, out, nq, n_own, kv_pre=None, n_pre=0, vis=None, s
 
 # ------------------------------------------------------- paged K/V cache ----
 
-def _here(t, name):
-    """Refuse a tensor of another device than the current one (pointers are
-    taken on the current device)."""
+# The calls below are made once per layer and token, so their checks read
+# each property of a tensor once (a call of a kernel of a few microseconds
+# must not wait for its Python side).
+
+def _paged_env(stream):
+    """(torch, current device, raw stream) of a call."""
+    import torch
+    dev = torch.cuda.current_device()
+    if stream is not None:
+        return torch, dev, stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    return torch, dev, raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
+
+
+def _refuse_device(t, dev, name):
     torch = _torch()
     if not isinstance(t, torch.Tensor) or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA tensor")
-    if t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name} is on {t.device}, the current device is cuda:{torch.cuda.current_device()}")
-    return t
+    raise ValueError(f"{name} is on {t.device}, the current device is cuda:{dev}")
 
 
-def _heads_view(t, dim, name):
-    """(pointer, row stride) of a [rows, heads, dim] tensor whose rows may
-    lie apart and whose heads are dense."""
-    _here(t, name)
-    if t.dim() != 3 or t.shape[2] != dim:
-        raise ValueError(f"{name} must be [rows, heads, {dim}], got {tuple(t.shape)}")
-    wide = t.shape[1] * dim
-    if t.numel() and (t.stride(2) != 1 or (t.shape[1] > 1 and t.stride(1) != dim)):
+def _rows_view(t, Tensor, dev, dim, name):
+    """(pointer, row stride, rows, heads) of a [rows, heads, dim] tensor on
+    the current device whose rows may lie apart and whose heads are dense."""
+    if not isinstance(t, Tensor) or t.get_device() != dev:
+        _refuse_device(t, dev, name)
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != dim:
+        raise ValueError(f"{name} must be [rows, heads, {dim}], got {tuple(shape)}")
+    rows, heads, _ = shape
+    wide = heads * dim
+    ld, sh, se = t.stride()
+    if rows and wide and (se != 1 or (heads > 1 and sh != dim)):
         raise ValueError(f"{name}: the heads of a row must be dense")
-    if t.shape[0] > 1 and t.stride(0) < wide:
+    if rows <= 1:
+        ld = max(ld, wide) if ld % 8 == 0 else wide
+    elif ld < wide:
         raise ValueError(f"{name}: rows overlap")
-    return t.data_ptr(), t.stride(0) if t.shape[0] > 1 else wide
+    return t.data_ptr(), ld, rows, heads
 
 
-def _flat(t, dtype, n, name):
+def _array(t, Tensor, dev, dtype, n, name):
     """Pointer of a contiguous tensor of n elements on the current device."""
     if t is None:
         return None
-    _here(t, name)
+    if not isinstance(t, Tensor) or t.get_device() != dev:
+        _refuse_device(t, dev, name)
+    if t.dtype != dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
     if t.numel() != n:
         raise ValueError(f"{name} must have {n} elements, got {t.numel()}")
-    return _ptr(t, dtype, name)
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
+    return t.data_ptr()
 
 
 def _elem(t):
     torch = _torch()
-    e = {torch.float32: B.ELEM_F32, torch.float16: B.ELEM_F16, torch.bfloat16: B.ELEM_BF16}.get(t.dtype)
+    e = {torch.bfloat16: B.ELEM_BF16, torch.float16: B.ELEM_F16, torch.float32: B.ELEM_F32}.get(t.dtype)
     if e is None:
         raise TypeError(f"expected an f32, f16 or bf16 tensor, got {t.dtype}")
     return e
@@ -546,18 +567,22 @@ def op_rope(r: Rope, x, pos, out=None, grad=False, stream=None):
     lie apart, as in a panel) turned by pos (int64 [rows], or [rows, 3] with
     three axes) into out (None: in place); grad=True turns a gradient back.
     Returns the output."""
-    torch = _torch()
-    px, ldx = _heads_view(x, r.head_dim, "x")
-    if out is None:
-        out = x
-    po, ldo = _heads_view(out, r.head_dim, "out")
-    if out.shape != x.shape or out.dtype != x.dtype:
-        raise ValueError("out must have x's shape and dtype")
-    if x.shape[1] == 0:
+    torch, dev, st = _paged_env(stream)
+    T = torch.Tensor
+    dim = r.head_dim
+    px, ldx, rows, heads = _rows_view(x, T, dev, dim, "x")
+    if out is None or out is x:
+        out, po, ldo = x, px, ldx
+    else:
+        po, ldo, orows, oheads = _rows_view(out, T, dev, dim, "out")
+        if orows != rows or oheads != heads or out.dtype != x.dtype:
+            raise ValueError("out must have x's shape and dtype")
+    if heads == 0:
         return out
-    check(load().qi21_op_rope(C.byref(r), _elem(x), x.shape[0], x.shape[1], px, ldx, po, ldo,
-                              _flat(pos, torch.int64, x.shape[0] * r.naxes, "pos"), 1 if grad else 0,
-                              _stream(stream)))
+    rc = load().qi21_op_rope(r, _elem(x), rows, heads, px, ldx, po, ldo,
+                             _array(pos, T, dev, torch.int64, rows * r.naxes, "pos"), 1 if grad else 0, st)
+    if rc:
+        check(rc)
     return out
 
 
@@ -569,21 +594,21 @@ class PagedKV:
     Keeps the tensors alive; their contents are read when the work runs."""
 
     def __init__(self, pool, table, lens, cu, prefix_pages=None, prefix_len=0):
-        torch = _torch()
-        _here(pool, "pool")
+        torch, dev, _ = _paged_env(None)
+        T = torch.Tensor
+        c = B.Paged()
+        c.pool = _array(pool, T, dev, getattr(pool, "dtype", None), pool.numel(), "pool")
         if pool.dim() != 5 or pool.shape[2] != 2:
             raise ValueError(f"pool must be [npages, page_rows, 2, kv_heads, head_dim], got {tuple(pool.shape)}")
         if table.dim() != 2:
             raise ValueError("table must be [nseq, pages]")
         nseq, stride = table.shape
-        c = B.Paged()
         c.dtype = _dt_code(pool)
-        c.pool = _ptr(pool, pool.dtype, "pool")
         c.npages, c.page_rows, _, c.kv_heads, c.head_dim = pool.shape
         c.nseq, c.table_stride = nseq, stride
-        c.table = _flat(table, torch.int32, nseq * stride, "table")
-        c.lens = _flat(lens, torch.int32, nseq, "lens")
-        c.cu = _flat(cu, torch.int32, nseq + 1, "cu")
+        c.table = _array(table, T, dev, torch.int32, nseq * stride, "table")
+        c.lens = _array(lens, T, dev, torch.int32, nseq, "lens")
+        c.cu = _array(cu, T, dev, torch.int32, nseq + 1, "cu")
         c.prefix_len = prefix_len
         if prefix_len > 0:
             if prefix_pages is None:
@@ -591,26 +616,39 @@ class PagedKV:
             need = -(-prefix_len // c.page_rows) if c.page_rows else 0
             if prefix_pages.numel() < need:
                 raise ValueError(f"prefix_pages must have {need} entries, got {prefix_pages.numel()}")
-            c.prefix_pages = _flat(prefix_pages, torch.int32, prefix_pages.numel(), "prefix_pages")
+            c.prefix_pages = _array(prefix_pages, T, dev, torch.int32, prefix_pages.numel(), "prefix_pages")
         self.c = c
+        self.device = dev
+        self.dtype = pool.dtype
         self._keep = (pool, table, lens, cu, prefix_pages)
+
+
+def _check_cache(kv, dev):
+    if kv.device != dev:
+        raise ValueError(f"the cache is on cuda:{kv.device}, the current device is cuda:{dev}")
 
 
 def op_kv_append(kv: PagedKV, k, v, rope=None, pos=None, stream=None):
     """qi21_op_kv_append: new keys (turned by rope at pos, int64; None: the
     rows' places in their sequences) and values, each [rows, kv_heads,
     head_dim], to their pages."""
-    torch = _torch()
+    torch, dev, st = _paged_env(stream)
+    T = torch.Tensor
     c = kv.c
-    pk, ldk = _heads_view(k, c.head_dim, "k")
-    pv, ldv = _heads_view(v, c.head_dim, "v")
-    if k.shape != v.shape or k.shape[1] != c.kv_heads:
-        raise ValueError(f"k and v must be [rows, {c.kv_heads}, {c.head_dim}]")
-    if _dt_code(k) != c.dtype or _dt_code(v) != c.dtype:
+    _check_cache(kv, dev)
+    dim = c.head_dim
+    pk, ldk, rows, heads = _rows_view(k, T, dev, dim, "k")
+    pv, ldv, vrows, vheads = _rows_view(v, T, dev, dim, "v")
+    if heads != c.kv_heads or vrows != rows or vheads != heads:
+        raise ValueError(f"k and v must be [rows, {c.kv_heads}, {dim}]")
+    if k.dtype != kv.dtype or v.dtype != kv.dtype:
         raise TypeError("k and v must have the pool's dtype")
-    n = k.shape[0] * (rope.naxes if rope is not None else 1)
-    check(load().qi21_op_kv_append(C.byref(c), k.shape[0], pk, ldk, pv, ldv, C.byref(rope) if rope is not None else None,
-                                   _flat(pos, torch.int64, n, "pos"), _stream(stream)))
+    pp = None
+    if pos is not None:
+        pp = _array(pos, T, dev, torch.int64, rows * (1 if rope is None else rope.naxes), "pos")
+    rc = load().qi21_op_kv_append(c, rows, pk, ldk, pv, ldv, rope, pp, st)
+    if rc:
+        check(rc)
 
 
 def attention_paged_bytes(kv: PagedKV, rows: int, heads: int) -> int:
@@ -626,20 +664,24 @@ def op_attention_paged(kv: PagedKV, q, out, workspace, causal=True, vis=None, sc
     [prefix, own rows] of their sequences into out; scale defaults to
     1 / sqrt(head_dim). vis int32 [rows] (read as unsigned): leading runs in
     place of the causal ones."""
-    torch = _torch()
+    torch, dev, st = _paged_env(stream)
+    T = torch.Tensor
     c = kv.c
-    pq, ldq = _heads_view(q, c.head_dim, "q")
-    po, ldo = _heads_view(out, c.head_dim, "out")
-    if out.shape != q.shape:
+    _check_cache(kv, dev)
+    dim = c.head_dim
+    pq, ldq, rows, heads = _rows_view(q, T, dev, dim, "q")
+    po, ldo, orows, oheads = _rows_view(out, T, dev, dim, "out")
+    if orows != rows or oheads != heads:
         raise ValueError("out must have q's shape")
-    if _dt_code(q) != c.dtype or _dt_code(out) != c.dtype:
+    if q.dtype != kv.dtype or out.dtype != kv.dtype:
         raise TypeError("q and out must have the pool's dtype")
-    _here(workspace, "workspace")
-    check(load().qi21_op_attention_paged(C.byref(c), q.shape[0], q.shape[1], pq, ldq, po, ldo, 1 if causal else 0,
-                                         _flat(vis, torch.int32, q.shape[0], "vis"),
-                                         c.head_dim ** -0.5 if scale is None else scale,
-                                         _ptr(workspace, None, "workspace"),
-                                         workspace.numel() * workspace.element_size(), _stream(stream)))
+    nws = workspace.numel() * workspace.element_size()
+    pw = _array(workspace, T, dev, workspace.dtype, workspace.numel(), "workspace")
+    pvis = None if vis is None else _array(vis, T, dev, torch.int32, rows, "vis")
+    rc = load().qi21_op_attention_paged(c, rows, heads, pq, ldq, po, ldo, 1 if causal else 0, pvis,
+                                        dim ** -0.5 if scale is None else scale, pw, nws, st)
+    if rc:
+        check(rc)
 
 
 def selftest_wait_timeout(stream=None):
