@@ -69,247 +69,251 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // ------------------------------------------------------- few rows a tile --
-// A CTA takes a tile of 16 MT (row, head) pairs of one key head and a run of
-// keys, the prefix's or a sequence's own. Its four warps take granules of 16
-// keys in turn, each through a ring of its own (16-byte asynchronous copies,
-// rows behind the end filled with zeros), so no warp waits for another: a
-// granule is Q K^T, the running maximum and sum, and P V, by m16n8k16 MMAs
-// with P taken from the score registers. The warps' parts are joined at the
-// end. It is bound by the bytes of K and V: a tile has few rows, so the
-// 128-row tensor-core tiles would be nearly empty.
+// A CTA takes a tile of 16 (row, head) pairs of one key head and a part of
+// the keys, the prefix's or a sequence's own. Its four warps take granules
+// of 16 keys in turn, each through a ring of its own (16-byte asynchronous
+// copies, rows behind the end filled with zeros), so no warp waits for
+// another: a granule is Q K^T, the running maximum and sum, and P V, by
+// m16n8k16 MMAs with P taken from the score registers. The warps' parts are
+// joined at the end. It is bound by the bytes of K and V: a tile has few
+// rows, so the 128-row tensor-core tiles would be nearly empty. Two stages a
+// warp rather than three leave room for three CTAs on an SM, whose starts
+// and ends overlap.
 template <int D>
-constexpr int kNarrowStages = D == 128 ? 3 : 4;
+constexpr int kNarrowStages = D == 128 ? 2 : 3;
 template <int D>
 constexpr int kNarrowSmem = kWarps * kNarrowStages<D> * 2 * kGran * D * 2;
 
-template <bool BF, int D, int MT>
+template <bool BF, int D>
 __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_constant__ PagedAttnArgs a) {
-  constexpr int R = 16 * MT;
   constexpr int NST = kNarrowStages<D>;
   constexpr int HALF = kGran * D * 2;  // bytes of a granule's K (or V)
   constexpr int CH = D / 8;            // 16-byte pieces of a row
+  constexpr int RS = 32 / CH;          // rows that a warp copies at once
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][R], s_l[kWarps][R];
+  __shared__ float s_m[kWarps][16], s_l[kWarps][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int hk = blockIdx.y;
-  int x = blockIdx.x;
+  // the key heads of a tile run side by side: their rows share DRAM pages
+  const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.kv.kv_heads));
+  int x = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.kv.kv_heads));
+  // the call's first kernel waits for what came before the call. A later one
+  // reads nothing of the kernel before it, so only its last CTA waits, at its
+  // end: the join waits for this kernel alone, which must end after that one
+  const bool waits = !a.first && blockIdx.x == gridDim.x - 1;
+  if (a.first) grid_wait();
+  grid_release();
 
-  // the tile: pairs [r0, r0 + nr) of the rows [t0, ...), the keys' source
-  // and their number for each row
+  // the tile: pairs [r0, npairs) of the rows [t0, ...), the keys' source and
+  // their number for each row
   const bool pre = x < a.pre_tiles * a.pre_splits;
-  int t0 = 0, npairs, r0, split, nsplit, slot, len = 0, nrows = 0;
-  const int32_t* pages;
   const int P = a.kv.prefix_len;
+  int t0 = 0, npairs, r0, split, slot, len = 0, nrows = 0;
+  const int32_t* pages;
   if (pre) {
     const int tile = x / a.pre_splits;
     split = x - tile * a.pre_splits;
-    nsplit = a.pre_splits;
     slot = split;
     pages = a.kv.prefix_pages;
     npairs = min(max(__ldg(a.kv.cu + a.kv.nseq), 0), a.rows) * a.group;
-    r0 = tile * R;
+    r0 = tile * 16;
   } else {
     x -= a.pre_tiles * a.pre_splits;
     const int tile = x / a.own_splits;
     split = x - tile * a.own_splits;
-    nsplit = a.own_splits;
     slot = a.pre_splits + split;
-    int b, at;
-    warp_find_tile(a, tile, a.group, R, lane, b, at);
-    if (b >= a.kv.nseq) return;
-    t0 = __ldg(a.kv.cu + b);
-    nrows = seq_rows(a, b);
-    npairs = nrows * a.group;
-    r0 = at * R;
-    pages = a.kv.table + static_cast<int64_t>(b) * a.kv.table_stride;
-    len = __ldg(a.kv.lens + b);
-    if ((len < nrows || len > a.kv.table_rows) && threadIdx.x == 0) atomicOr(&s_paged_status, kStatusPage);
+    const SeqTile q = warp_find_tile(a, tile, a.group, 16, lane);
+    t0 = q.row0;
+    nrows = q.rows;
+    npairs = nrows * a.group;  // 0 if there is no such tile
+    r0 = q.at * 16;
+    pages = a.kv.table + static_cast<int64_t>(q.b) * a.kv.table_stride;
+    len = q.len;
+    if (npairs > 0 && (len < nrows || len > a.kv.table_rows) && threadIdx.x == 0) atomicOr(&s_paged_status, kStatusPage);
     len = min(max(len, 0), a.kv.table_rows);
   }
-  if (r0 >= npairs) return;
+  if (r0 >= npairs) {
+    if (waits) grid_wait();
+    return;
+  }
 
-  // this thread's rows: lane / 4 and + 8 of each 16-row tile
+  // this thread's rows: lane / 4 and + 8
   const int tq = lane >> 2, tj = lane & 3;
-  int lim[MT][2];  // keys of this part that the row sees
-  uint32_t qf[MT][D / 16][4];
-  int most = 0;
+  int lim[2];  // keys of this source that the row sees
+  uint32_t qf[D / 16][4];
+  int most = 0, least = 0x7fffffff;
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      const int pr = r0 + mt * 16 + tq + 8 * e;
-      const bool live = pr < npairs;
-      const int i = live ? pr / a.group : 0;
-      const int t = t0 + i;
-      const int h = hk * a.group + (live ? pr - i * a.group : 0);
-      int n = 0;
-      if (live) {
-        if (pre)
-          n = a.vis ? static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(P))) : P;
-        else if (a.vis)
-          n = static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(P) + len)) - P;
-        else
-          n = a.causal ? len - nrows + i + 1 : len;
-        n = min(max(n, 0), pre ? P : len);
-      }
-      lim[mt][e] = n;
-      most = max(most, n);
-      const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
-                                                             static_cast<int64_t>(t) * a.ldq + h * D);
-#pragma unroll
-      for (int k = 0; k < D / 16; ++k) {
-        qf[mt][k][e] = live ? __ldg(qr + 8 * k + tj) : 0u;
-        qf[mt][k][2 + e] = live ? __ldg(qr + 8 * k + 4 + tj) : 0u;
-      }
+  for (int e = 0; e < 2; ++e) {
+    const int pr = r0 + tq + 8 * e;
+    const bool live = pr < npairs;
+    const int i = live ? pr / a.group : 0;
+    const int t = t0 + i;
+    const int h = hk * a.group + (live ? pr - i * a.group : 0);
+    int n = 0;
+    if (live) {
+      if (pre)
+        n = a.vis ? static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(P))) : P;
+      else if (a.vis)
+        n = static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(P) + len)) - P;
+      else
+        n = a.causal ? len - nrows + i + 1 : len;
+      n = min(max(n, 0), pre ? P : len);
+      least = min(least, n);
     }
+    lim[e] = n;
+    most = max(most, n);
+    const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
+                                                           static_cast<int64_t>(t) * a.ldq + h * D);
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    for (int k = 0; k < D / 16; ++k) {
+      qf[k][e] = live ? __ldg(qr + 8 * k + tj) : 0u;
+      qf[k][2 + e] = live ? __ldg(qr + 8 * k + 4 + tj) : 0u;
+    }
+  }
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
+  }
 
-  // this warp's granules of the split: g0, g0 + 4, ... below g1
-  const int ng = (most + kGran - 1) / kGran;
-  const int g0 = static_cast<int>(static_cast<int64_t>(ng) * split / nsplit) + warp;
-  const int g1 = static_cast<int>(static_cast<int64_t>(ng) * (split + 1) / nsplit);
-  const uint8_t* ring = smem + warp * (NST * 2 * HALF);
-  const uint32_t sring = smem_u32(ring);
-  const uint16_t* pool = static_cast<const uint16_t*>(a.kv.pool);
-  const int64_t row_elems = 2 * static_cast<int64_t>(a.kv.kv_heads) * D;
-
+  // this warp's granules of the part: g0, g0 + 4, ... below g1
+  const int part = pre ? a.pre_keys : a.own_keys;  // a multiple of a granule
+  const int64_t k0 = static_cast<int64_t>(split) * part;
+  const int g0 = static_cast<int>(min(k0, static_cast<int64_t>(most)) / kGran) + warp;
+  const int g1 = static_cast<int>((min(k0 + part, static_cast<int64_t>(most)) + kGran - 1) / kGran);
+  const bool any = k0 < most;
+  const uint32_t sring = smem_u32(smem) + warp * (NST * 2 * HALF);
+  const int64_t row_bytes = 4 * static_cast<int64_t>(a.kv.kv_heads) * D;
+  const int64_t v_off = 2 * static_cast<int64_t>(a.kv.kv_heads) * D;
+  // copies: a lane moves piece cp_c of rows cp_r, cp_r + RS, ...
+  const int cp_r = lane / CH, cp_c = lane % CH;
+  const uint8_t* cp_src = static_cast<const uint8_t*>(a.kv.pool) + hk * (2 * D) + cp_c * 16 + cp_r * row_bytes;
   auto page_of = [&](int g) { return __ldg(pages + g * kGran / a.kv.page_rows); };
   auto fetch = [&](int g, int id, int st) {
     const bool ok = id >= 0 && id < a.kv.npages;
     if (!ok && lane == 0) atomicOr(&s_paged_status, kStatusPage);
+    const int left = ok ? most - g * kGran : 0;  // rows before the end
     const int64_t row = static_cast<int64_t>(ok ? id : 0) * a.kv.page_rows + g * kGran % a.kv.page_rows;
-    const uint16_t* base = pool + row * row_elems + hk * D;
-    const uint32_t d0 = sring + st * 2 * HALF;
+    const uint8_t* src = cp_src + row * row_bytes;
+    const uint32_t dst = sring + st * 2 * HALF + cp_r * (D * 2);
+    if (left >= kGran) {
 #pragma unroll
-    for (int i = 0; i < 2 * kGran * CH / 32; ++i) {
-      const int u = i * 32 + lane;
-      const int kv = u / (kGran * CH), w = u % (kGran * CH);
-      const int r = w / CH, c = w % CH;
-      const bool live = ok && g * kGran + r < most;
-      const uint16_t* src = live ? base + r * row_elems + (kv ? a.kv.kv_heads * D : 0) + c * 8 : pool;
-      cp_async16(d0 + kv * HALF + r * (D * 2) + ((c ^ (r & 7)) << 4), src, live);
+      for (int i = 0; i < kGran / RS; ++i) {
+        const uint32_t d = dst + i * (RS * D * 2) + ((cp_c ^ ((cp_r + i * RS) & 7)) << 4);
+        cp_async16(d, src, true);
+        cp_async16(d + HALF, src + v_off, true);
+        src += RS * row_bytes;
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < kGran / RS; ++i) {
+        const uint32_t d = dst + i * (RS * D * 2) + ((cp_c ^ ((cp_r + i * RS) & 7)) << 4);
+        const bool live = cp_r + i * RS < left;
+        cp_async16(d, live ? src : cp_src, live);
+        cp_async16(d + HALF, live ? src + v_off : cp_src, live);
+        src += RS * row_bytes;
+      }
     }
   };
 
-  float o[MT][D / 8][4];
-  float m[MT][2], l[MT][2];
+  float o[D / 8][4];
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt) {
+  for (int n = 0; n < D / 8; ++n)
 #pragma unroll
-    for (int n = 0; n < D / 8; ++n)
-#pragma unroll
-      for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
-    m[mt][0] = m[mt][1] = -INFINITY;
-    l[mt][0] = l[mt][1] = 0.f;
-  }
+    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-  int nf = g0;  // next granule to fetch
+  int nf = any ? g0 : g1;  // next granule to fetch
   int nid = nf < g1 ? page_of(nf) : 0;
-#pragma unroll
-  for (int s = 0; s < NST - 1; ++s) {
+  auto fetch_next = [&](int st) {
     if (nf < g1) {
       const int id = nid, g = nf;
       nf += kWarps;
       if (nf < g1) nid = page_of(nf);
-      fetch(g, id, s);
+      fetch(g, id, st);
     }
     cp_async_commit();
-  }
+  };
+#pragma unroll
+  for (int s = 0; s < NST - 1; ++s) fetch_next(s);
   int st = 0;
-  for (int g = g0; g < g1; g += kWarps) {
+  // matrix addresses of this lane: K by rows (lane % 8 and the upper half),
+  // V by rows for the transposed load
+  const int kkey = (lane >> 4) * 8 + (lane & 7), kbit = (lane >> 3) & 1;
+  const int vkey = ((lane >> 3) & 1) * 8 + (lane & 7), vbit = lane >> 4;
+  const uint32_t kx = (kbit ^ (kkey & 7)) << 4, vx = (vbit ^ (vkey & 7)) << 4;
+  const float c = a.scale_log2;
+  for (int g = any ? g0 : g1; g < g1; g += kWarps) {
     cp_async_wait<NST - 2>();
     __syncwarp();
     {
       int fs = st + NST - 1;
       if (fs >= NST) fs -= NST;
-      if (nf < g1) {
-        const int id = nid, gg = nf;
-        nf += kWarps;
-        if (nf < g1) nid = page_of(nf);
-        fetch(gg, id, fs);
-      }
-      cp_async_commit();
+      fetch_next(fs);
     }
-    const uint32_t sk = sring + st * 2 * HALF, sv = sk + HALF;
+    const uint32_t sk = sring + st * 2 * HALF + kkey * (D * 2), sv = sring + st * 2 * HALF + HALF + vkey * (D * 2);
     if (++st == NST) st = 0;
 
-    float s[MT][2][4];
+    float s[2][4];
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt)
+    for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
+      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       uint32_t b[4];
-      const int key = (lane >> 4) * 8 + (lane & 7), c = 2 * k + ((lane >> 3) & 1);
-      ldsm4<false>(sk + key * (D * 2) + ((c ^ (key & 7)) << 4), b);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma16816<BF>(s[mt][0], qf[mt][k], b[0], b[1]);
-        mma16816<BF>(s[mt][1], qf[mt][k], b[2], b[3]);
-      }
+      ldsm4<false>(sk + (kx ^ (k << 5)), b);
+      mma16816<BF>(s[0], qf[k], b[0], b[1]);
+      mma16816<BF>(s[1], qf[k], b[2], b[3]);
     }
-    uint32_t p[MT][4];
+    if (g * kGran + kGran > least) {  // what a row does not see is taken out
+      const int col = g * kGran + 2 * tj;
 #pragma unroll
-    for (int mt = 0; mt < MT; ++mt) {
-      float al[2];
-      bool moved = false;
+      for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // scores in log2 units; what the row does not see is taken out
-        float mx = -INFINITY;
+        for (int e = 0; e < 4; ++e)
+          if (col + 8 * n + (e & 1) >= lim[e >> 1]) s[n][e] = -INFINITY;
+    }
+    uint32_t p[4];
+    float al[2];
+    bool moved = false;
 #pragma unroll
-        for (int n = 0; n < 2; ++n)
-#pragma unroll
-          for (int c = 0; c < 2; ++c) {
-            float& v = s[mt][n][2 * e + c];
-            v = g * kGran + 8 * n + 2 * tj + c < lim[mt][e] ? v * a.scale_log2 : -INFINITY;
-            mx = fmaxf(mx, v);
-          }
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-        // the maximum is raised only past the threshold: o and l share it
-        al[e] = 1.f;
-        if (mx > m[mt][e] + kPagedRescale) {
-          al[e] = ex2(m[mt][e] - mx);
-          m[mt][e] = mx;
-          moved = true;
-        }
-        const float base = m[mt][e] == -INFINITY ? 0.f : m[mt][e];
-        float sum = 0.f;
-#pragma unroll
-        for (int n = 0; n < 2; ++n) {
-          const float p0 = ex2(s[mt][n][2 * e] - base), p1 = ex2(s[mt][n][2 * e + 1] - base);
-          sum += p0 + p1;
-          // P is rounded to the values' type for the MMA (half a step of a
-          // weight each, of either sign); l sums the f32 weights
-          p[mt][2 * n + e] = pack2<BF>(p0, p1);
-        }
-        l[mt][e] = l[mt][e] * al[e] + sum;
+    for (int e = 0; e < 2; ++e) {
+      float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * c;
+      // the maximum (log2 units) is raised only past the threshold: o and l
+      // share it
+      al[e] = 1.f;
+      if (mx > m[e] + kPagedRescale) {
+        al[e] = ex2(m[e] - mx);
+        m[e] = mx;
+        moved = true;
       }
-      if (__any_sync(0xffffffffu, moved)) {
+      // a row that has seen no key yet has weights 2^(-inf - 0) = 0
+      const float base = m[e] == -INFINITY ? 0.f : -m[e];
+      const float p0 = ex2(fmaf(s[0][2 * e], c, base)), p1 = ex2(fmaf(s[0][2 * e + 1], c, base));
+      const float p2 = ex2(fmaf(s[1][2 * e], c, base)), p3 = ex2(fmaf(s[1][2 * e + 1], c, base));
+      // P is rounded to the values' type for the MMA (half a step of a
+      // weight each, of either sign); l sums the f32 weights
+      p[e] = pack2<BF>(p0, p1);
+      p[2 + e] = pack2<BF>(p2, p3);
+      l[e] = fmaf(l[e], al[e], (p0 + p1) + (p2 + p3));
+    }
+    if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-        for (int n = 0; n < D / 8; ++n) {
-          o[mt][n][0] *= al[0];
-          o[mt][n][1] *= al[0];
-          o[mt][n][2] *= al[1];
-          o[mt][n][3] *= al[1];
-        }
+      for (int n = 0; n < D / 8; ++n) {
+        o[n][0] *= al[0];
+        o[n][1] *= al[0];
+        o[n][2] *= al[1];
+        o[n][3] *= al[1];
       }
     }
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) {
       uint32_t b[4];
-      const int key = ((lane >> 3) & 1) * 8 + (lane & 7), c = 2 * n + (lane >> 4);
-      ldsm4<true>(sv + key * (D * 2) + ((c ^ (key & 7)) << 4), b);
-#pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma16816<BF>(o[mt][2 * n], p[mt], b[0], b[1]);
-        mma16816<BF>(o[mt][2 * n + 1], p[mt], b[2], b[3]);
-      }
+      ldsm4<true>(sv + (vx ^ (n << 5)), b);
+      mma16816<BF>(o[2 * n], p, b[0], b[1]);
+      mma16816<BF>(o[2 * n + 1], p, b[2], b[3]);
     }
     __syncwarp();  // the stage is refilled next round
   }
@@ -317,34 +321,30 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
 
   // join the four warps: each leaves its sums in its ring
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float sum = l[mt][e];
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-      if (tj == 0) {
-        s_m[warp][mt * 16 + tq + 8 * e] = m[mt][e];
-        s_l[warp][mt * 16 + tq + 8 * e] = sum;
-      }
+  for (int e = 0; e < 2; ++e) {
+    float sum = l[e];
+    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+    if (tj == 0) {
+      s_m[warp][tq + 8 * e] = m[e];
+      s_l[warp][tq + 8 * e] = sum;
     }
+  }
   constexpr int OP = D + 4;  // row pitch of the f32 sums: spreads the rows over the banks
-  static_assert(16 * MT * OP * 4 <= NST * 2 * HALF, "the sums fit the ring");
+  static_assert(16 * OP * 4 <= NST * 2 * HALF, "the sums fit the ring");
   float* so = reinterpret_cast<float*>(smem + warp * (NST * 2 * HALF));
   __syncwarp();
 #pragma unroll
-  for (int mt = 0; mt < MT; ++mt)
-#pragma unroll
-    for (int n = 0; n < D / 8; ++n) {
-      *reinterpret_cast<float2*>(so + (mt * 16 + tq) * OP + 8 * n + 2 * tj) = make_float2(o[mt][n][0], o[mt][n][1]);
-      *reinterpret_cast<float2*>(so + (mt * 16 + tq + 8) * OP + 8 * n + 2 * tj) = make_float2(o[mt][n][2], o[mt][n][3]);
-    }
+  for (int n = 0; n < D / 8; ++n) {
+    *reinterpret_cast<float2*>(so + tq * OP + 8 * n + 2 * tj) = make_float2(o[n][0], o[n][1]);
+    *reinterpret_cast<float2*>(so + (tq + 8) * OP + 8 * n + 2 * tj) = make_float2(o[n][2], o[n][3]);
+  }
   __syncthreads();
   constexpr int TR = D / 4;  // threads of a row, 4 values each
-  for (int r = threadIdx.x / TR; r < R; r += kWarps * 32 / TR) {
+  for (int r = threadIdx.x / TR; r < 16; r += kWarps * 32 / TR) {
     const int pr = r0 + r;
     if (pr >= npairs) break;
-    const int c = (threadIdx.x % TR) * 4;
+    const int col = (threadIdx.x % TR) * 4;
     float mm = -INFINITY;
 #pragma unroll
     for (int w = 0; w < kWarps; ++w) mm = fmaxf(mm, s_m[w][r]);
@@ -355,7 +355,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     for (int w = 0; w < kWarps; ++w) {
       const float f = ex2(s_m[w][r] - base);
       const float4 v = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(smem + w * (NST * 2 * HALF)) + r * OP + c);
+          reinterpret_cast<const float*>(smem + w * (NST * 2 * HALF)) + r * OP + col);
       ll += f * s_l[w][r];
       acc.x += f * v.x;
       acc.y += f * v.y;
@@ -366,14 +366,15 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     const int t = t0 + i, h = hk * a.group + pr - i * a.group;
     if (a.slots == 1) {
       const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;  // a row that sees no key is 0
-      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + t * a.ldo + h * D + c);
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + t * a.ldo + h * D + col);
       *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF>(acc.x * inv, acc.y * inv), pack2<BF>(acc.z * inv, acc.w * inv));
     } else {
       const int64_t at = (static_cast<int64_t>(slot) * a.rows + t) * a.heads + h;
-      *reinterpret_cast<float4*>(a.part_o + at * D + c) = acc;
-      if (c == 0) a.part_ml[at] = make_float2(mm, ll);
+      if (any) *reinterpret_cast<float4*>(a.part_o + at * D + col) = acc;  // without keys its weight is 0
+      if (col == 0) a.part_ml[at] = make_float2(mm, ll);
     }
   }
+  if (waits) grid_wait();
 }
 
 // ----------------------------------------------------------------- join --
@@ -384,6 +385,7 @@ template <bool BF, int D>
 __global__ void __launch_bounds__(256) attn_paged_join(const __grid_constant__ PagedAttnArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t pair = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  grid_wait();
   const int64_t pairs = static_cast<int64_t>(min(max(__ldg(a.kv.cu + a.kv.nseq), 0), a.rows)) * a.heads;
   if (pair >= pairs) return;
   const int64_t step = static_cast<int64_t>(a.rows) * a.heads;
@@ -403,22 +405,27 @@ __global__ void __launch_bounds__(256) attn_paged_join(const __grid_constant__ P
       ll += w * ml.y;
     }
     const int n = min(32, a.slots - s0);
-#pragma unroll 4
-    for (int s = 0; s < n; ++s) {
-      const float ws = __shfl_sync(0xffffffffu, w, s);
-      if (ws == 0.f) continue;  // a part without keys may hold no sums
-      const float* src = a.part_o + ((s0 + s) * step + pair) * D + lane * V;
-      if (V == 4) {
-        const float4 v = *reinterpret_cast<const float4*>(src);
-        acc[0] += ws * v.x;
-        acc[1] += ws * v.y;
-        acc[2 % V] += ws * v.z;
-        acc[3 % V] += ws * v.w;
-      } else {
-        const float2 v = *reinterpret_cast<const float2*>(src);
-        acc[0] += ws * v.x;
-        acc[1] += ws * v.y;
+    for (int s = 0; s < n; s += 8) {
+      float ws[8];
+      alignas(16) float v[8][V];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        ws[k] = __shfl_sync(0xffffffffu, w, (s + k) & 31);
+        if (s + k >= n) ws[k] = 0.f;
+#pragma unroll
+        for (int i = 0; i < V; ++i) v[k][i] = 0.f;
+        if (ws[k] != 0.f) {  // a part without keys may hold no sums
+          const float* src = a.part_o + ((s0 + s + k) * step + pair) * D + lane * V;
+          if constexpr (V == 4)
+            *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
+          else
+            *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
+        }
       }
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+#pragma unroll
+        for (int i = 0; i < V; ++i) acc[i] += ws[k] * v[k][i];
     }
   }
 #pragma unroll
@@ -464,12 +471,29 @@ static int wide_splits(int64_t items, int64_t blocks, int64_t slots, int64_t row
   return best;
 }
 
+// A launch that may start while the kernel before it in the stream runs
+// (grid_wait inside it).
+static cudaError_t launch_early(void (*kernel)(PagedAttnArgs), unsigned grid, unsigned threads, size_t smem,
+                                cudaStream_t s, const PagedAttnArgs& a) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kernel, a);
+}
+
 template <bool BF, int D>
 static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   constexpr int smem = kNarrowSmem<D>;
   static PerDevice<cudaError_t> once;
   const cudaError_t* attr = once.get([] {
-    return cudaFuncSetAttribute(attn_paged_narrow<BF, D, 1>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return cudaFuncSetAttribute(attn_paged_narrow<BF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
   });
   if (attr == nullptr) return cudaErrorNoDevice;
   if (*attr != cudaSuccess) return *attr;
@@ -480,8 +504,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   const int tokens = a.kv.npages > 0 ? wide_tokens(a.group) : 0;
   cudaError_t e = cudaSuccess;
   auto join = [&] {
-    attn_paged_join<BF, D><<<static_cast<unsigned>((all + 7) / 8), 256, 0, s>>>(a);
-    return cudaGetLastError();
+    return launch_early(attn_paged_join<BF, D>, static_cast<unsigned>((all + 7) / 8), 256, 0, s, a);
   };
   auto place_parts = [&] {
     a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.slots) * a.rows * a.heads * D);
@@ -502,12 +525,14 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   // sequence's own keys for its own
   const int R = 16;
   a.own_tiles = static_cast<int>(pairs / R + seqs);
-  // narrow splits: enough CTAs for two waves of two per SM, none of fewer
-  // than 256 keys
-  const int64_t want = 4 * static_cast<int64_t>(sm_count());
-  auto splits = [&](int64_t tiles, int64_t keys, int cap) {
-    const int64_t n = std::min<int64_t>((want + tiles * hk - 1) / (tiles * hk), (keys + 255) / 256);
-    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, cap)));
+  // parts of the few-row tiles: enough CTAs for two waves of three per SM,
+  // none of fewer than 256 keys
+  const int64_t want = 6 * static_cast<int64_t>(sm_count());
+  auto splits = [&](int64_t tiles, int64_t keys, int cap, int* part) {
+    int64_t n = std::min<int64_t>((want + tiles * hk - 1) / (tiles * hk), (keys + 255) / 256);
+    n = std::max<int64_t>(1, std::min<int64_t>(n, cap));
+    *part = static_cast<int>(((keys + n - 1) / n + kGran - 1) / kGran * kGran);
+    return static_cast<int>(n);
   };
   const bool wide = P > 0 && tokens > 0 && pairs > R;
   const bool pair = D == 128 && pairs > 128;
@@ -519,16 +544,17 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
                                sm_count() / (pair ? 2 : 1), all, D, most - 1);
   } else if (P > 0) {
     a.pre_tiles = static_cast<int>((pairs + R - 1) / R);
-    a.pre_splits = splits(a.pre_tiles, P, most - 1);
+    a.pre_splits = splits(a.pre_tiles, P, most - 1, &a.pre_keys);
   }
-  a.own_splits = splits(a.own_tiles, a.kv.table_rows, most - a.pre_splits);
+  a.own_splits = splits(a.own_tiles, a.kv.table_rows, most - a.pre_splits, &a.own_keys);
   a.slots = a.pre_splits + a.own_splits;
   place_parts();
   if (wide && (e = launch_attn_wide(a, WIDE_PREFIX, pair, wide_tiles, a.pre_splits, s)) != cudaSuccess) return e;
-  const int64_t gx = static_cast<int64_t>(a.pre_tiles) * a.pre_splits + static_cast<int64_t>(a.own_tiles) * a.own_splits;
+  const int64_t gx = hk * (static_cast<int64_t>(a.pre_tiles) * a.pre_splits +
+                           static_cast<int64_t>(a.own_tiles) * a.own_splits);
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
-  attn_paged_narrow<BF, D, 1><<<dim3(static_cast<unsigned>(gx), hk), kWarps * 32, smem, s>>>(a);
-  e = cudaGetLastError();
+  a.first = !wide;
+  e = launch_early(attn_paged_narrow<BF, D>, static_cast<unsigned>(gx), kWarps * 32, smem, s, a);
   return e != cudaSuccess || a.slots == 1 ? e : join();
 }
 

@@ -92,20 +92,21 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
   const int tile = item % p.tiles, split = item / p.tiles;
   const int P = a.kv.prefix_len;
 
+  grid_wait();
+  grid_release();
   // the item: tokens [tok0, tok_end) of this CTA's tile and the keys that its
   // (and its pair's) rows see at most
   int tok0, tok_end, len = 0, nrows = 0, seq0 = 0;
   const int32_t* own_pages = nullptr;
   if (p.joint) {
-    int b, at;
-    warp_find_tile(a, tile, 1, CT * p.tokens, lane, b, at);
-    if (b >= a.kv.nseq) return;
-    seq0 = __ldg(a.kv.cu + b);
-    nrows = seq_rows(a, b);
-    tok0 = seq0 + at * CT * p.tokens;
+    const SeqTile q = warp_find_tile(a, tile, 1, CT * p.tokens, lane);
+    if (q.b >= a.kv.nseq) return;
+    seq0 = q.row0;
+    nrows = q.rows;
+    tok0 = seq0 + q.at * CT * p.tokens;
     tok_end = seq0 + nrows;
-    own_pages = a.kv.table + static_cast<int64_t>(b) * a.kv.table_stride;
-    len = __ldg(a.kv.lens + b);
+    own_pages = a.kv.table + static_cast<int64_t>(q.b) * a.kv.table_stride;
+    len = q.len;
     if ((len < nrows || len > a.kv.table_rows) && threadIdx.x == 0) atomicOr(&s_wide_status, kStatusPage);
     len = min(max(len, 0), a.kv.table_rows);
   } else {
@@ -625,13 +626,15 @@ static cudaError_t launch_wide_t(const WideArgs& w, cudaStream_t s) {
   cfg.blockDim = dim3(kWThreads);
   cfg.dynamicSmemBytes = W::kSmem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
-  at[0].id = cudaLaunchAttributeClusterDimension;
-  at[0].val.clusterDim.x = PAIR ? 2 : 1;
-  at[0].val.clusterDim.y = 1;
-  at[0].val.clusterDim.z = 1;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = PAIR ? 2 : 1;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = PAIR ? 1 : 0;
+  cfg.numAttrs = PAIR ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, attn_paged_wide<BF, D, PAIR>, w);
 }
 

@@ -54,28 +54,36 @@ struct PagedAttnArgs {
   int causal;
   const uint32_t* vis;
   float scale_log2;
-  int pre_tiles, pre_splits;  // CTAs of the prefix: tiles x splits
+  int pre_tiles, pre_splits;  // few-row tiles of the prefix, and the parts of its keys
   int own_tiles, own_splits;
+  int pre_keys, own_keys;     // keys of a few-row part
+  int first;                  // this kernel is the call's first
   int slots;                  // parts per row; 1: the part is the result
   float* part_o;              // [slots][rows][heads][dim]
   float2* part_ml;            // [slots][rows][heads] (max in log2 units, sum)
 };
 
-// New rows of sequence b: 0 for ends that do not fit the call's rows.
-__device__ __forceinline__ int seq_rows(const PagedAttnArgs& a, int b) {
-  const int c0 = __ldg(a.kv.cu + b), c1 = __ldg(a.kv.cu + b + 1);
-  return (c0 >= 0 && c1 <= a.rows && c1 > c0) ? c1 - c0 : 0;
-}
-
 // The x-th tile, counted over the sequences in order, of `tile` of the `per`
-// pieces that a row has: its sequence and its place there, by one whole
-// warp (32 sequences per round). b == nseq: there are fewer tiles.
-__device__ __forceinline__ void warp_find_tile(const PagedAttnArgs& a, int x, int per, int tile, int lane, int& b,
-                                               int& at) {
+// pieces that a row has: its sequence b and its place `at` there, the
+// sequence's first row and rows in this call, and its length as given; by
+// one whole warp (32 sequences per round, all of their numbers loaded at
+// once). b == nseq: there are fewer tiles.
+struct SeqTile {
+  int b, at, row0, rows, len;
+};
+__device__ __forceinline__ SeqTile warp_find_tile(const PagedAttnArgs& a, int x, int per, int tile, int lane) {
+  SeqTile r{a.kv.nseq, 0, 0, 0, 0};
   int before = 0;
   for (int b0 = 0; b0 < a.kv.nseq; b0 += 32) {
-    int n = 0;
-    if (b0 + lane < a.kv.nseq) n = (seq_rows(a, b0 + lane) * per + tile - 1) / tile;
+    int c0 = 0, rows = 0, len = 0;
+    if (b0 + lane < a.kv.nseq) {
+      c0 = __ldg(a.kv.cu + b0 + lane);
+      len = __ldg(a.kv.lens + b0 + lane);
+      const int c1 = __ldg(a.kv.cu + b0 + lane + 1);
+      // ends that do not fit the call's rows: no rows
+      rows = (c0 >= 0 && c1 <= a.rows && c1 > c0) ? c1 - c0 : 0;
+    }
+    const int n = (rows * per + tile - 1) / tile;
     int sum = n;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -85,15 +93,23 @@ __device__ __forceinline__ void warp_find_tile(const PagedAttnArgs& a, int x, in
     const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
     if (past) {
       const int l = __ffs(past) - 1;
-      b = b0 + l;
-      at = x - before - __shfl_sync(0xffffffffu, sum - n, l);
-      return;
+      r.b = b0 + l;
+      r.at = x - before - __shfl_sync(0xffffffffu, sum - n, l);
+      r.row0 = __shfl_sync(0xffffffffu, c0, l);
+      r.rows = __shfl_sync(0xffffffffu, rows, l);
+      r.len = __shfl_sync(0xffffffffu, len, l);
+      return r;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
-  b = a.kv.nseq;
-  at = 0;
+  return r;
 }
+
+// Programmatic launch: a call's kernels may start while the one before them
+// in the stream still runs. grid_wait returns when that one has ended and
+// its writes are visible; grid_release lets the next one start.
+__device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
 // Tiles of many rows on the tensor cores (k_paged_tc.cu).
 enum WideMode : int { WIDE_PREFIX = 0, WIDE_JOINT = 1 };
