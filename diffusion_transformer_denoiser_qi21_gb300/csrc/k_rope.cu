@@ -10,6 +10,7 @@
 // is off by 0.03 rad). cos and sin are then taken in f32 of the remainder
 // of at most an eighth of a turn either way.
 #include <algorithm>
+#include <cstring>
 #include <type_traits>
 
 #include "internal.h"
@@ -28,21 +29,11 @@ unsigned int rope_status_read_clear() {
 }
 
 constexpr int kRopeThreads = 256;
-constexpr int kRopeBatch = 4;        // units in flight per thread
+// heads in flight per thread: 64 bytes of 16-byte pieces
+template <bool HALF>
+constexpr int kRopeBatch = HALF ? 2 : 4;
 constexpr int kRopeMaxCs = 4096;     // (cos, sin) pairs of a CTA: 32 KB
 constexpr int kRopeMaxRows = 64;     // rows of a CTA
-
-// Division by an invariant d < 2^20 of n < 2^20: n * ceil(2^40 / d) >> 40
-// (the multiplier is over by less than 1, so the quotient by less than
-// n / 2^40 < 1 / d: exact).
-struct FastDiv {
-  uint64_t m;
-  uint32_t d;
-};
-static FastDiv fast_div(uint32_t d) { return FastDiv{((1ull << 40) + d - 1) / d, d}; }
-__device__ __forceinline__ uint32_t div_by(uint32_t n, const FastDiv& f) {
-  return static_cast<uint32_t>((n * f.m) >> 40);
-}
 
 struct RopeArgs {
   RopeDev r;
@@ -51,11 +42,12 @@ struct RopeArgs {
   const void* v;  // append only
   int64_t ldx, ldo, ldv;
   const int64_t* pos;
-  int rows, heads, dim, rpc;  // rpc: rows of a CTA
-  int head_units, v_units;    // units of a head of x, 16-byte (or smaller) pieces of a head of v
-  float sgn;                  // -1 for the gradient
-  FastDiv by_row, by_head;
-  PagedArgs p;  // append only
+  int rows, heads, dim;
+  int rpc;         // rows of a CTA
+  int units;       // of a head (see the kernel)
+  int head_lanes;  // threads that share a row's column piece
+  float sgn;       // -1 for the gradient
+  PagedArgs p;     // append only
 };
 
 template <typename T>
@@ -66,6 +58,18 @@ __device__ __forceinline__ float widen(T v) {
     return __bfloat162float(v);
   else
     return v;
+}
+// Two neighbouring values of a piece, rounded together: one conversion of
+// both runs at the arithmetic rate, two single ones at a quarter of it.
+template <typename T>
+__device__ __forceinline__ void put2(T* e, float lo, float hi) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t w = pack2<std::is_same<T, __nv_bfloat16>::value>(lo, hi);
+    memcpy(e, &w, 4);
+  } else {
+    e[0] = lo;
+    e[1] = hi;
+  }
 }
 template <typename T>
 __device__ __forceinline__ T narrow(float v) {
@@ -118,154 +122,203 @@ __device__ __forceinline__ float2 cos_sin_turns(uint64_t turns) {
   return make_float2((qd + 1) & 2 ? -cc : cc, qd & 2 ? -ss : ss);
 }
 
-// A CTA takes rpc rows; a thread walks units of them, kRopeBatch at a time
-// with the loads of a batch ahead of its arithmetic (the first batch's ahead
-// of the angles too). A unit is one piece of E values of a head, or in the
-// HALF layout of the turned part the two pieces whose values pair up. The
-// rows' (cos, sin) are made once per row and shared by its heads.
-// What bounds it: the bytes of x and out; the angles cost rot / 2 of about
-// 40 instructions per row.
+// The places of rows [row0, row0 + n) in the cache, n <= 64, by one warp: the
+// first row's sequence by a search of all of them, the others' by a search
+// of the next 32 sequences' numbers, held by the lanes (and of all where that
+// is short).
+__device__ __forceinline__ void append_places(const PagedArgs& p, int row0, int n, int lane, int64_t* dst, int64_t* pos) {
+  const int b0 = warp_find_seq(p.cu, p.nseq, row0, lane);
+  const bool is = b0 + lane < p.nseq;
+  const int beg = is ? __ldg(p.cu + b0 + lane) : 0x7fffffff;
+  const int end = is ? __ldg(p.cu + b0 + lane + 1) : 0x7fffffff;
+  const int len = is ? __ldg(p.lens + b0 + lane) : 0;
+  for (int base = 0; base < n; base += 32) {
+    const int t = row0 + base + lane;
+    int k = 0;  // ends that are <= t, of the 32
+#pragma unroll
+    for (int s = 16; s > 0; s >>= 1)
+      if (__shfl_sync(0xffffffffu, end, k + s - 1) <= t) k += s;
+    const bool past = __shfl_sync(0xffffffffu, end, 31) <= t;
+    const int c0 = __shfl_sync(0xffffffffu, beg, k);  // of the row's sequence b0 + k
+    const int c1 = __shfl_sync(0xffffffffu, end, k);
+    int b = c0 <= t && t < c1 ? b0 + k : p.nseq;
+    int own = __shfl_sync(0xffffffffu, len, k) - (c1 - t);
+    for (unsigned left = __ballot_sync(0xffffffffu, past && base + lane < n); left; left &= left - 1) {
+      const int l = __ffs(left) - 1;
+      const int at = warp_find_seq(p.cu, p.nseq, row0 + base + l, lane);
+      if (lane == l) {
+        b = at;
+        if (b < p.nseq) own = __ldg(p.lens + b) - (__ldg(p.cu + b + 1) - t);
+      }
+    }
+    if (base + lane < n) {
+      dst[base + lane] = b < p.nseq ? paged_row(p, b, own, &s_rope_status) : -1;
+      pos[base + lane] = static_cast<int64_t>(p.prefix_len) + own;
+    }
+  }
+}
+
+// A CTA takes rpc rows. A head is cut into units: one piece of E values, or
+// in the HALF layout's turned part the two pieces whose values pair up. A
+// thread has one unit of every head_lanes-th head of a row (of the keys'
+// heads, then the values' in an append), so it reads the (cos, sin) of its
+// columns once per row and turns several heads with them. kRopeBatch heads
+// are loaded ahead of their arithmetic, the first ones ahead of the angles,
+// and four CTAs share an SM. What bounds it: the bytes of x and out. 32768
+// rows of 32 heads of 128 (bf16, 537 MB): 88 us, 6.1 TB/s; with (cos, sin)
+// read per head, conflicting banks and the frequencies read per angle, 118.
 template <typename T, bool HALF, int E, bool VECT, bool APPEND>
-__global__ void __launch_bounds__(kRopeThreads) rope_kernel(const __grid_constant__ RopeArgs a) {
-  extern __shared__ float2 cs[];  // [rpc][rot / 2]
+__global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
+  extern __shared__ __align__(16) float cs[];  // [rpc][cos, sin][rot / 2]
   __shared__ int64_t s_dst[kRopeMaxRows];  // append: row of the pool, or -1
   __shared__ int64_t s_pos[kRopeMaxRows];  // append without positions: the row's
+  using P = Piece<T, E, VECT>;
+  constexpr int Z = HALF ? E : (E + 1) / 2;  // pairs of a unit
+  constexpr int NB = kRopeBatch<HALF>;
   const int tid = threadIdx.x;
   const int row0 = static_cast<int>(blockIdx.x) * a.rpc;
   const int nrow = min(a.rpc, a.rows - row0);
   const int hp = a.r.rot >> 1;
-  const uint32_t per_row = a.by_row.d;  // units of a row (x, then v)
-  const uint32_t total = static_cast<uint32_t>(nrow) * per_row;
-  const uint32_t xu = static_cast<uint32_t>(a.heads) * a.head_units;  // units of x in a row
-  const int turn_units = HALF ? hp / E : (a.r.rot + E - 1) / E;       // those of a head that turn
+  const int heads = APPEND ? 2 * a.heads : a.heads;
 
-  using P = Piece<T, E, VECT>;
-  struct Where {
-    int row, col, kind;  // kind 0: turned, 1: copied, 2: v copied
-    int c;               // first column within the head
-  };
-  auto locate = [&](uint32_t u) {
-    Where w;
-    w.row = static_cast<int>(div_by(u, a.by_row));
-    const uint32_t q = u - static_cast<uint32_t>(w.row) * per_row;
-    if (!APPEND || q < xu) {
-      const uint32_t h = div_by(q, a.by_head);
-      const int i = static_cast<int>(q - h * a.head_units);
-      if (i < turn_units) {
-        w.kind = 0;
-        w.c = i * E;
-      } else {
-        w.kind = 1;
-        w.c = HALF ? a.r.rot + (i - turn_units) * E : i * E;
-      }
-      w.col = static_cast<int>(h) * a.dim + w.c;
-    } else {
-      const uint32_t q2 = q - xu;
-      w.kind = 2;
-      w.c = 0;
-      w.col = static_cast<int>(q2) * E;
-    }
-    return w;
-  };
-  auto load = [&](const Where& w, P& p0, P& p1) {
-    const T* src = w.kind == 2 ? static_cast<const T*>(a.v) + (row0 + w.row) * a.ldv + w.col
-                               : static_cast<const T*>(a.x) + (row0 + w.row) * a.ldx + w.col;
-    p0.load(src);
-    if (HALF && w.kind == 0) p1.load(src + hp);
-  };
+  // this thread's unit and its first row and head
+  const int tpr = a.units * a.head_lanes;  // threads of a row
+  const int step = kRopeThreads / tpr;     // rows at once
+  const int first = tid / tpr;
+  const int lane_h = (tid - first * tpr) / a.units;
+  const int unit = tid - first * tpr - lane_h * a.units;
+  const int turn_units = HALF ? hp / E : (a.r.rot + E - 1) / E;
+  const bool turns = unit < turn_units;
+  const int col = turns || !HALF ? unit * E : a.r.rot + (unit - turn_units) * E;
+  const int live = a.r.rot - col;  // values of an interleaved piece that turn
+  const bool two = HALF && turns;
+  const bool active = first < step;
 
-  P b0[kRopeBatch], b1[kRopeBatch];
-  Where at[kRopeBatch];
+  P b0[NB], b1[NB];
+  auto load = [&](int row, int h0) {
 #pragma unroll
-  for (int i = 0; i < kRopeBatch; ++i) {
-    const uint32_t u = tid + i * kRopeThreads;
-    if (u < total) {
-      at[i] = locate(u);
-      load(at[i], b0[i], b1[i]);
+    for (int k = 0; k < NB; ++k) {
+      const int h = h0 + k * a.head_lanes;
+      if (h < heads) {
+        const T* src = APPEND && h >= a.heads
+                           ? static_cast<const T*>(a.v) + row * a.ldv + (h - a.heads) * a.dim + col
+                           : static_cast<const T*>(a.x) + row * a.ldx + h * a.dim + col;
+        b0[k].load(src);
+        if (two) b1[k].load(src + hp);
+      }
     }
-  }
+  };
+  if (active && first < nrow) load(row0 + first, lane_h);
 
   if (APPEND) {
-    const int warp = tid >> 5, lane = tid & 31;
-    for (int r = warp; r < nrow; r += kRopeThreads / 32) {
-      const int t = row0 + r;
-      const int b = warp_find_seq(a.p.cu, a.p.nseq, t, lane);
-      if (lane == 0) {
-        int64_t dst = -1;
-        int own = 0;
-        if (b < a.p.nseq) {
-          own = __ldg(a.p.lens + b) - (__ldg(a.p.cu + b + 1) - t);
-          dst = paged_row(a.p, b, own, &s_rope_status);
-        }
-        s_dst[r] = dst;
-        s_pos[r] = static_cast<int64_t>(a.p.prefix_len) + own;
-      }
-    }
+    if (tid < 32) append_places(a.p, row0, nrow, tid, s_dst, s_pos);
     if (a.pos == nullptr) __syncthreads();
   }
-  for (int i = tid; i < nrow * hp; i += kRopeThreads) {
-    const int r = i / hp, j = i - r * hp;
-    const int64_t ps = APPEND && a.pos == nullptr
-                           ? s_pos[r]
-                           : __ldg(reinterpret_cast<const long long*>(a.pos) +
-                                   static_cast<int64_t>(row0 + r) * a.r.naxes + a.r.axis[j]);
-    const float2 z = cos_sin_turns(static_cast<uint64_t>(ps) * a.r.turns[j]);
-    cs[i] = make_float2(z.x * a.r.scale, z.y * a.r.scale * a.sgn);
-  }
-  __syncthreads();
-
-  for (uint32_t u0 = tid; u0 < total; u0 += kRopeBatch * kRopeThreads) {
-    if (u0 != static_cast<uint32_t>(tid)) {
-#pragma unroll
-      for (int i = 0; i < kRopeBatch; ++i) {
-        const uint32_t u = u0 + i * kRopeThreads;
-        if (u < total) {
-          at[i] = locate(u);
-          load(at[i], b0[i], b1[i]);
-        }
+  // a thread keeps one pair: its frequency is read once (the parameter
+  // memory serves lanes that read different words one after the other)
+  if (hp > 0) {
+    const int r1 = tid / hp, j = tid - r1 * hp;
+    if (r1 < kRopeThreads / hp) {
+      const uint64_t turns_j = a.r.turns[j];
+      const int axis = a.r.axis[j];
+      // a unit of 8 pairs is read as two pieces of 4: the pieces of
+      // neighbouring units side by side keep the reads off each other's banks
+      const int at = Z == 8 ? ((j & 4 ? turn_units : 0) + (j >> 3)) * 4 + (j & 3) : j;
+      for (int r = r1; r < nrow; r += kRopeThreads / hp) {
+        const int64_t ps = APPEND && a.pos == nullptr
+                               ? s_pos[r]
+                               : __ldg(reinterpret_cast<const long long*>(a.pos) +
+                                       static_cast<int64_t>(row0 + r) * a.r.naxes + axis);
+        const float2 z = cos_sin_turns(static_cast<uint64_t>(ps) * turns_j);
+        cs[r * 2 * hp + at] = z.x * a.r.scale;
+        cs[r * 2 * hp + at + hp] = z.y * a.r.scale * a.sgn;
       }
     }
+  }
+  __syncthreads();
+  if (!active) return;
+
+  for (int r = first; r < nrow; r += step) {
+    alignas(16) float zc[Z], zs[Z];
+    if (turns) {
+      if constexpr (Z >= 4) {
+        const float* src = cs + r * 2 * hp + unit * 4;
+        if (HALF || live >= E) {
+          // hp and with it every address is a multiple of 4 values here: in
+          // the HALF layout by the choice of E, else if the head turns whole
+          // units (a unit that turns in part reads its pairs one by one)
 #pragma unroll
-    for (int i = 0; i < kRopeBatch; ++i) {
-      if (u0 + i * kRopeThreads >= total) break;
-      const Where& w = at[i];
-      T* dst;
-      if (APPEND) {
-        const int64_t row = s_dst[w.row];
-        if (row < 0) continue;
-        dst = static_cast<T*>(a.out) + row * a.ldo + (w.kind == 2 ? a.heads * a.dim : 0) + w.col;
-      } else {
-        dst = static_cast<T*>(a.out) + (row0 + w.row) * a.ldo + w.col;
-      }
-      if (w.kind == 0) {
-        const float2* z = cs + w.row * hp + (HALF ? w.c : w.c / 2);
-        if constexpr (HALF) {
-          P o0, o1;
+          for (int i = 0; i < Z; i += 4) {
+            if ((hp & 3) == 0) {
+              *reinterpret_cast<float4*>(zc + i) = *reinterpret_cast<const float4*>(src + i * turn_units);
+              *reinterpret_cast<float4*>(zs + i) = *reinterpret_cast<const float4*>(src + hp + i * turn_units);
+            } else {
 #pragma unroll
-          for (int e = 0; e < E; ++e) {
-            const float p = widen(b0[i].e[e]), q = widen(b1[i].e[e]);
-            const float2 g = z[e];
-            o0.e[e] = narrow<T>(p * g.x - q * g.y);
-            o1.e[e] = narrow<T>(p * g.y + q * g.x);
-          }
-          o0.store(dst);
-          o1.store(dst + hp);
-        } else {
-          P o = b0[i];
-          const int live = a.r.rot - w.c;  // the rest of the piece does not turn
-#pragma unroll
-          for (int e = 0; e + 1 < E; e += 2) {
-            if (e < live) {
-              const float p = widen(b0[i].e[e]), q = widen(b0[i].e[e + 1]);
-              const float2 g = z[e / 2];
-              o.e[e] = narrow<T>(p * g.x - q * g.y);
-              o.e[e + 1] = narrow<T>(p * g.y + q * g.x);
+              for (int k = 0; k < 4; ++k) {
+                zc[i + k] = src[i * turn_units + k];
+                zs[i + k] = src[hp + i * turn_units + k];
+              }
             }
           }
-          o.store(dst);
+        } else {
+#pragma unroll
+          for (int k = 0; k < Z; ++k)
+            if (2 * k < live) {
+              zc[k] = src[k];
+              zs[k] = src[hp + k];
+            }
         }
       } else {
-        b0[i].store(dst);
+        const float* src = cs + r * 2 * hp + unit * Z;
+#pragma unroll
+        for (int k = 0; k < Z; ++k)
+          if (HALF || 2 * k < live) {
+            zc[k] = src[k];
+            zs[k] = src[hp + k];
+          }
+      }
+    }
+    T* dst0;
+    if (APPEND) {
+      dst0 = static_cast<T*>(a.out) + s_dst[r] * a.ldo + col;
+      if (s_dst[r] < 0) dst0 = nullptr;
+    } else {
+      dst0 = static_cast<T*>(a.out) + (row0 + r) * a.ldo + col;
+    }
+    for (int h0 = lane_h; h0 < heads; h0 += NB * a.head_lanes) {
+      if (r != first || h0 != lane_h) load(row0 + r, h0);
+#pragma unroll
+      for (int k = 0; k < NB; ++k) {
+        const int h = h0 + k * a.head_lanes;
+        if (h >= heads || (APPEND && dst0 == nullptr)) break;
+        T* dst = dst0 + h * a.dim;  // the values' heads follow the keys' in a cache row
+        if (turns && !(APPEND && h >= a.heads)) {
+          if constexpr (HALF) {
+            if constexpr (E == 1) {
+              const float p = widen(b0[k].e[0]), q = widen(b1[k].e[0]);
+              b0[k].e[0] = narrow<T>(p * zc[0] - q * zs[0]);
+              b1[k].e[0] = narrow<T>(p * zs[0] + q * zc[0]);
+            } else {
+#pragma unroll
+              for (int e = 0; e < E; e += 2) {
+                const float p0 = widen(b0[k].e[e]), q0 = widen(b1[k].e[e]);
+                const float p1 = widen(b0[k].e[e + 1]), q1 = widen(b1[k].e[e + 1]);
+                put2(&b0[k].e[e], p0 * zc[e] - q0 * zs[e], p1 * zc[e + 1] - q1 * zs[e + 1]);
+                put2(&b1[k].e[e], p0 * zs[e] + q0 * zc[e], p1 * zs[e + 1] + q1 * zc[e + 1]);
+              }
+            }
+          } else {
+#pragma unroll
+            for (int e = 0; e + 1 < E; e += 2) {
+              if (e < live) {
+                const float p = widen(b0[k].e[e]), q = widen(b0[k].e[e + 1]);
+                put2(&b0[k].e[e], p * zc[e / 2] - q * zs[e / 2], p * zs[e / 2] + q * zc[e / 2]);
+              }
+            }
+          }
+        }
+        b0[k].store(dst);
+        if (two) b1[k].store(dst + hp);
       }
     }
   }
@@ -275,22 +328,26 @@ template <typename T, bool HALF, int E, bool VECT, bool APPEND>
 static cudaError_t launch_t(RopeArgs& a, bool inplace, cudaStream_t s) {
   const int hp = a.r.rot / 2;
   if (HALF)
-    a.head_units = hp / E + (inplace ? 0 : (a.dim - a.r.rot) / E);
+    a.units = hp / E + (inplace ? 0 : (a.dim - a.r.rot) / E);
   else
-    a.head_units = inplace ? (a.r.rot + E - 1) / E : a.dim / E;
-  a.v_units = APPEND ? a.dim / E : 0;
-  const int64_t per_row = static_cast<int64_t>(a.heads) * (a.head_units + a.v_units);
-  a.by_row = fast_div(static_cast<uint32_t>(per_row));
-  a.by_head = fast_div(static_cast<uint32_t>(a.head_units));
-  // rows of a CTA: about two batches of units per thread, fewer while that
-  // would leave SMs without a CTA, and no more than the (cos, sin) room
-  int64_t rpc = 2 * kRopeBatch * kRopeThreads / per_row;
-  rpc = std::min<int64_t>(rpc, a.rows / (2 * sm_count()));
+    a.units = inplace ? (a.r.rot + E - 1) / E : a.dim / E;
+  const int heads = APPEND ? 2 * a.heads : a.heads;
+  // one batch of heads per thread and row; calls of few rows spread a row
+  // over all threads of a CTA
+  const int few = 2 * sm_count();
+  const int lanes = a.rows < few ? heads : (heads + kRopeBatch<HALF> - 1) / kRopeBatch<HALF>;
+  a.head_lanes = std::max(1, std::min(lanes, kRopeThreads / a.units));
+  const int at_once = kRopeThreads / (a.units * a.head_lanes);
+  // rows of a CTA: four rounds of its threads (an append's search and the
+  // angles are paid once per CTA), fewer while that would leave SMs idle,
+  // and no more than the (cos, sin) room
+  int64_t rpc = static_cast<int64_t>(at_once) * 4;
+  rpc = std::min<int64_t>(rpc, a.rows / few);
   if (hp > 0) rpc = std::min<int64_t>(rpc, kRopeMaxCs / hp);
   a.rpc = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rpc, kRopeMaxRows)));
   const unsigned grid = static_cast<unsigned>((a.rows + static_cast<int64_t>(a.rpc) - 1) / a.rpc);
   rope_kernel<T, HALF, E, VECT, APPEND>
-      <<<grid, kRopeThreads, static_cast<size_t>(a.rpc) * hp * sizeof(float2), s>>>(a);
+      <<<grid, kRopeThreads, static_cast<size_t>(a.rpc) * hp * 2 * sizeof(float), s>>>(a);
   return cudaGetLastError();
 }
 
