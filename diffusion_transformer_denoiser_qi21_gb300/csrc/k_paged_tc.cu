@@ -89,59 +89,10 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
   const int hk = blockIdx.y;
   constexpr int CT = PAIR ? 2 : 1;  // CTAs (tiles) of an item
   const int item = static_cast<int>(blockIdx.x) / CT;
-  const int tile = item % p.tiles, split = item / p.tiles;
+  // a sequence's last tiles see the most keys: they start first, so that the
+  // last wave of CTAs is of short ones
+  const int tile = p.tiles - 1 - item % p.tiles, split = item / p.tiles;
   const int P = a.kv.prefix_len;
-
-  grid_wait();
-  grid_release();
-  // the item: tokens [tok0, tok_end) of this CTA's tile and the keys that its
-  // (and its pair's) rows see at most
-  int tok0, tok_end, len = 0, nrows = 0, seq0 = 0;
-  const int32_t* own_pages = nullptr;
-  if (p.joint) {
-    const SeqTile q = warp_find_tile(a, tile, 1, CT * p.tokens, lane);
-    if (q.b >= a.kv.nseq) return;
-    seq0 = q.row0;
-    nrows = q.rows;
-    tok0 = seq0 + q.at * CT * p.tokens;
-    tok_end = seq0 + nrows;
-    own_pages = a.kv.table + static_cast<int64_t>(q.b) * a.kv.table_stride;
-    len = q.len;
-    if ((len < nrows || len > a.kv.table_rows) && threadIdx.x == 0) atomicOr(&s_wide_status, kStatusPage);
-    len = min(max(len, 0), a.kv.table_rows);
-  } else {
-    tok0 = tile * CT * p.tokens;
-    tok_end = min(max(__ldg(a.kv.cu + a.kv.nseq), 0), a.rows);
-    if (tok0 >= tok_end) return;
-  }
-  // keys of [prefix, own] that token t sees
-  const int total = P + len;
-  auto limit = [&](int t) {
-    int n = total;
-    if (a.vis)
-      n = static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(total)));
-    else if (a.causal && p.joint)
-      n = P + min(max(len - nrows + (t - seq0) + 1, 0), len);
-    return n;
-  };
-  const int item_end = min(tok_end, tok0 + CT * p.tokens);
-  int most;
-  if (a.vis) {
-    most = 0;
-    for (int t = tok0 + lane; t < item_end; t += 32) most = max(most, limit(t));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-  } else {
-    most = limit(item_end - 1);
-  }
-  tok0 += rank * p.tokens;
-  // key blocks: the prefix's, then the own keys'; this split's are [j0, j1)
-  const int np = min(most, P), no = max(most - P, 0);
-  const int npb = (np + kWK - 1) / kWK;
-  const int nb = npb + (no + kWK - 1) / kWK;
-  const int j0 = static_cast<int>(static_cast<int64_t>(nb) * split / p.splits);
-  const int j1 = static_cast<int>(static_cast<int64_t>(nb) * (split + 1) / p.splits);
-  const int n = j1 - j0;
 
   uint64_t* bars = reinterpret_cast<uint64_t*>(smem + W::kOffBar);
   uint64_t* qfull = bars;             // even CTA: both Q tiles landed
@@ -193,6 +144,57 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
   else
     __syncthreads();
   tc_fence_after();
+  // what came before the call is done from here on (the set-up above touches
+  // none of it); the call's next kernel may start
+  grid_wait();
+  grid_release();
+  // the item: tokens [tok0, tok_end) of this CTA's tile and the keys that its
+  // (and its pair's) rows see at most
+  int tok0 = 0, tok_end = 0, len = 0, nrows = 0, seq0 = 0;
+  const int32_t* own_pages = nullptr;
+  if (p.joint) {
+    const SeqTile q = warp_find_tile(a, tile, 1, CT * p.tokens, lane);
+    seq0 = q.row0;  // no such tile: no rows
+    nrows = q.rows;
+    tok0 = seq0 + q.at * CT * p.tokens;
+    tok_end = seq0 + nrows;
+    own_pages = a.kv.table + static_cast<int64_t>(q.b) * a.kv.table_stride;
+    len = q.len;
+    if (nrows > 0 && (len < nrows || len > a.kv.table_rows) && threadIdx.x == 0)
+      atomicOr(&s_wide_status, kStatusPage);
+    len = min(max(len, 0), a.kv.table_rows);
+  } else {
+    tok0 = tile * CT * p.tokens;
+    tok_end = min(max(__ldg(a.kv.cu + a.kv.nseq), 0), a.rows);
+  }
+  // keys of [prefix, own] that token t sees
+  const int total = P + len;
+  auto limit = [&](int t) {
+    int n = total;
+    if (a.vis)
+      n = static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(total)));
+    else if (a.causal && p.joint)
+      n = P + min(max(len - nrows + (t - seq0) + 1, 0), len);
+    return n;
+  };
+  const int item_end = min(tok_end, tok0 + CT * p.tokens);
+  int most = 0;
+  if (a.vis) {
+    for (int t = tok0 + lane; t < item_end; t += 32) most = max(most, limit(t));
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+  } else if (tok0 < item_end) {
+    most = limit(item_end - 1);
+  }
+  tok0 += rank * p.tokens;
+  // key blocks: the prefix's, then the own keys'; this split's are [j0, j1)
+  const int np = min(most, P), no = max(most - P, 0);
+  const int npb = (np + kWK - 1) / kWK;
+  const int nb = npb + (no + kWK - 1) / kWK;
+  const int j0 = static_cast<int>(static_cast<int64_t>(nb) * split / p.splits);
+  const int j1 = static_cast<int>(static_cast<int64_t>(nb) * (split + 1) / p.splits);
+  const int n = j1 - j0;
+
   const uint32_t tmem = *tslot;
   const uint32_t tS = tmem;        // S buffers at columns [0, 384)
   const uint32_t tO = tmem + 384;  // O at columns [384, 384 + D)
