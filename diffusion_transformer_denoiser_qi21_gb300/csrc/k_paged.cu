@@ -37,6 +37,21 @@ __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
+// Loads from the shared memory of a CTA of the cluster.
+__device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
+  float2 v;
+  asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+  return v;
+}
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr) {
+  float4 v;
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(addr)
+               : "memory");
+  return v;
+}
+
 template <bool TRANS>
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   if (TRANS)
@@ -79,10 +94,16 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 // rows, so the 128-row tensor-core tiles would be nearly empty. Two stages a
 // warp rather than three leave room for three CTAs on an SM, whose starts
 // and ends overlap.
+//
+// Small calls (a.cluster > 0) are one launch: a tile's CTAs walk [prefix, own
+// keys] of its sequence, split evenly over a cluster of up to eight that
+// joins its parts through distributed shared memory.
 template <int D>
 constexpr int kNarrowStages = D == 128 ? 2 : 3;
 template <int D>
-constexpr int kNarrowSmem = kWarps * kNarrowStages<D> * 2 * kGran * D * 2;
+constexpr int kNarrowRing = kWarps * kNarrowStages<D> * 2 * kGran * D * 2;
+template <int D>
+constexpr int kNarrowSmem = kNarrowRing<D> + 16 * (D * 4 + 8);  // a CTA's part: sums, then (max, sum)
 
 template <bool BF, int D>
 __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_constant__ PagedAttnArgs a) {
@@ -94,8 +115,10 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
   __shared__ float s_m[kWarps][16], s_l[kWarps][16];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the key heads of a tile run side by side: their rows share DRAM pages
-  const int hk = static_cast<int>(blockIdx.x % static_cast<unsigned>(a.kv.kv_heads));
-  int x = static_cast<int>(blockIdx.x / static_cast<unsigned>(a.kv.kv_heads));
+  const int ncl = max(1, a.cluster);
+  int x = static_cast<int>(blockIdx.x / static_cast<unsigned>(ncl));
+  const int hk = x % a.kv.kv_heads;
+  x /= a.kv.kv_heads;
   // the call's first kernel waits for what came before the call. A later one
   // reads nothing of the kernel before it, so only its last CTA waits, at its
   // end: the join waits for this kernel alone, which must end after that one
@@ -103,44 +126,45 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
   if (a.first) grid_wait();
   grid_release();
 
-  // the tile: pairs [r0, npairs) of the rows [t0, ...), the keys' source and
-  // their number for each row
+  // the tile: pairs [r0, npairs) of the rows [t0, ...) and the sources of its
+  // keys, the prefix (np rows), own keys (len rows) or both
   const bool pre = x < a.pre_tiles * a.pre_splits;
   const int P = a.kv.prefix_len;
+  const int np = pre || a.cluster ? P : 0;
   int t0 = 0, npairs, r0, split, slot, len = 0, nrows = 0;
-  const int32_t* pages;
+  const int32_t* own_pages = nullptr;
   if (pre) {
     const int tile = x / a.pre_splits;
     split = x - tile * a.pre_splits;
     slot = split;
-    pages = a.kv.prefix_pages;
     npairs = min(max(__ldg(a.kv.cu + a.kv.nseq), 0), a.rows) * a.group;
     r0 = tile * 16;
   } else {
     x -= a.pre_tiles * a.pre_splits;
     const int tile = x / a.own_splits;
-    split = x - tile * a.own_splits;
+    split = a.cluster ? static_cast<int>(cluster_rank()) : x - tile * a.own_splits;
     slot = a.pre_splits + split;
     const SeqTile q = warp_find_tile(a, tile, a.group, 16, lane);
     t0 = q.row0;
     nrows = q.rows;
     npairs = nrows * a.group;  // 0 if there is no such tile
     r0 = q.at * 16;
-    pages = a.kv.table + static_cast<int64_t>(q.b) * a.kv.table_stride;
+    own_pages = a.kv.table + static_cast<int64_t>(q.b) * a.kv.table_stride;
     len = q.len;
     if (npairs > 0 && (len < nrows || len > a.kv.table_rows) && threadIdx.x == 0) atomicOr(&s_paged_status, kStatusPage);
     len = min(max(len, 0), a.kv.table_rows);
   }
-  if (r0 >= npairs) {
+  if (r0 >= npairs) {  // all CTAs of a cluster
     if (waits) grid_wait();
     return;
   }
 
-  // this thread's rows: lane / 4 and + 8
+  // this thread's rows: lane / 4 and + 8; the keys that they see of the
+  // prefix and of the own ones, and the most and least of the tile
   const int tq = lane >> 2, tj = lane & 3;
-  int lim[2];  // keys of this source that the row sees
+  int lim_p[2], lim_o[2];
   uint32_t qf[D / 16][4];
-  int most = 0, least = 0x7fffffff;
+  int most_p = 0, most_o = 0, least_p = 0x7fffffff, least_o = 0x7fffffff;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int pr = r0 + tq + 8 * e;
@@ -148,19 +172,19 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     const int i = live ? pr / a.group : 0;
     const int t = t0 + i;
     const int h = hk * a.group + (live ? pr - i * a.group : 0);
-    int n = 0;
+    int n = P + len;  // of [prefix, own keys]
+    if (live && a.vis)
+      n = static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(n)));
+    else if (a.causal && !pre)
+      n = P + min(max(len - nrows + i + 1, 0), len);
+    lim_p[e] = live ? min(n, np) : 0;
+    lim_o[e] = live ? min(max(n - P, 0), len) : 0;
+    most_p = max(most_p, lim_p[e]);
+    most_o = max(most_o, lim_o[e]);
     if (live) {
-      if (pre)
-        n = a.vis ? static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(P))) : P;
-      else if (a.vis)
-        n = static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(P) + len)) - P;
-      else
-        n = a.causal ? len - nrows + i + 1 : len;
-      n = min(max(n, 0), pre ? P : len);
-      least = min(least, n);
+      least_p = min(least_p, lim_p[e]);
+      least_o = min(least_o, lim_o[e]);
     }
-    lim[e] = n;
-    most = max(most, n);
     const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
                                                            static_cast<int64_t>(t) * a.ldq + h * D);
 #pragma unroll
@@ -169,30 +193,43 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
       qf[k][2 + e] = live ? __ldg(qr + 8 * k + 4 + tj) : 0u;
     }
   }
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) {
-    most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
-    least = min(least, __shfl_xor_sync(0xffffffffu, least, o));
-  }
+  most_p = __reduce_max_sync(0xffffffffu, most_p);
+  most_o = __reduce_max_sync(0xffffffffu, most_o);
+  least_p = __reduce_min_sync(0xffffffffu, least_p);
+  least_o = __reduce_min_sync(0xffffffffu, least_o);
 
-  // this warp's granules of the part: g0, g0 + 4, ... below g1
-  const int part = pre ? a.pre_keys : a.own_keys;  // a multiple of a granule
-  const int64_t k0 = static_cast<int64_t>(split) * part;
-  const int g0 = static_cast<int>(min(k0, static_cast<int64_t>(most)) / kGran) + warp;
-  const int g1 = static_cast<int>((min(k0 + part, static_cast<int64_t>(most)) + kGran - 1) / kGran);
-  const bool any = k0 < most;
+  // granules: the prefix's, then the own keys'; this warp's are g0, g0 + 4,
+  // ... below g1
+  const int gp = (most_p + kGran - 1) / kGran;
+  const int ng = gp + (most_o + kGran - 1) / kGran;
+  int g0, g1;
+  if (a.cluster) {
+    g0 = static_cast<int>(static_cast<int64_t>(ng) * split / ncl);
+    g1 = static_cast<int>(static_cast<int64_t>(ng) * (split + 1) / ncl);
+  } else {
+    const int part = (pre ? a.pre_keys : a.own_keys) / kGran;
+    const int64_t k0 = static_cast<int64_t>(split) * part;
+    g0 = static_cast<int>(min(k0, static_cast<int64_t>(ng)));
+    g1 = static_cast<int>(min(k0 + part, static_cast<int64_t>(ng)));
+  }
+  const bool any = g0 < g1;
+  g0 += warp;
   const uint32_t sring = smem_u32(smem) + warp * (NST * 2 * HALF);
   const int64_t row_bytes = 4 * static_cast<int64_t>(a.kv.kv_heads) * D;
   const int64_t v_off = 2 * static_cast<int64_t>(a.kv.kv_heads) * D;
   // copies: a lane moves piece cp_c of rows cp_r, cp_r + RS, ...
   const int cp_r = lane / CH, cp_c = lane % CH;
   const uint8_t* cp_src = static_cast<const uint8_t*>(a.kv.pool) + hk * (2 * D) + cp_c * 16 + cp_r * row_bytes;
-  auto page_of = [&](int g) { return __ldg(pages + g * kGran / a.kv.page_rows); };
+  auto page_of = [&](int g) {
+    return g < gp ? __ldg(a.kv.prefix_pages + g * kGran / a.kv.page_rows)
+                  : __ldg(own_pages + (g - gp) * kGran / a.kv.page_rows);
+  };
   auto fetch = [&](int g, int id, int st) {
     const bool ok = id >= 0 && id < a.kv.npages;
     if (!ok && lane == 0) atomicOr(&s_paged_status, kStatusPage);
-    const int left = ok ? most - g * kGran : 0;  // rows before the end
-    const int64_t row = static_cast<int64_t>(ok ? id : 0) * a.kv.page_rows + g * kGran % a.kv.page_rows;
+    const int key = (g < gp ? g : g - gp) * kGran;
+    const int left = ok ? (g < gp ? most_p : most_o) - key : 0;  // rows before the end
+    const int64_t row = static_cast<int64_t>(ok ? id : 0) * a.kv.page_rows + key % a.kv.page_rows;
     const uint8_t* src = cp_src + row * row_bytes;
     const uint32_t dst = sring + st * 2 * HALF + cp_r * (D * 2);
     if (left >= kGran) {
@@ -222,7 +259,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
   float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
 
-  int nf = any ? g0 : g1;  // next granule to fetch
+  int nf = g0;  // next granule to fetch
   int nid = nf < g1 ? page_of(nf) : 0;
   auto fetch_next = [&](int st) {
     if (nf < g1) {
@@ -242,7 +279,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
   const int vkey = ((lane >> 3) & 1) * 8 + (lane & 7), vbit = lane >> 4;
   const uint32_t kx = (kbit ^ (kkey & 7)) << 4, vx = (vbit ^ (vkey & 7)) << 4;
   const float c = a.scale_log2;
-  for (int g = any ? g0 : g1; g < g1; g += kWarps) {
+  for (int g = g0; g < g1; g += kWarps) {
     cp_async_wait<NST - 2>();
     __syncwarp();
     {
@@ -265,8 +302,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
       mma16816<BF>(s[0], qf[k], b[0], b[1]);
       mma16816<BF>(s[1], qf[k], b[2], b[3]);
     }
-    if (g * kGran + kGran > least) {  // what a row does not see is taken out
-      const int col = g * kGran + 2 * tj;
+    const bool of_p = g < gp;
+    const int key = (of_p ? g : g - gp) * kGran;
+    if (key + kGran > (of_p ? least_p : least_o)) {  // what a row does not see is taken out
+      const int lim[2] = {of_p ? lim_p[0] : lim_o[0], of_p ? lim_p[1] : lim_o[1]};
+      const int col = key + 2 * tj;
 #pragma unroll
       for (int n = 0; n < 2; ++n)
 #pragma unroll
@@ -341,6 +381,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
   }
   __syncthreads();
   constexpr int TR = D / 4;  // threads of a row, 4 values each
+  float* part = reinterpret_cast<float*>(smem + kNarrowRing<D>);
+  float2* part_ml = reinterpret_cast<float2*>(part + 16 * D);
   for (int r = threadIdx.x / TR; r < 16; r += kWarps * 32 / TR) {
     const int pr = r0 + r;
     if (pr >= npairs) break;
@@ -362,6 +404,11 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
       acc.z += f * v.z;
       acc.w += f * v.w;
     }
+    if (ncl > 1) {
+      *reinterpret_cast<float4*>(part + r * D + col) = acc;
+      if (col == 0) part_ml[r] = make_float2(mm, ll);
+      continue;
+    }
     const int i = pr / a.group;
     const int t = t0 + i, h = hk * a.group + pr - i * a.group;
     if (a.slots == 1) {
@@ -373,6 +420,42 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
       if (any) *reinterpret_cast<float4*>(a.part_o + at * D + col) = acc;  // without keys its weight is 0
       if (col == 0) a.part_ml[at] = make_float2(mm, ll);
     }
+  }
+  if (ncl > 1) {
+    // the cluster's parts: CTA k finishes rows k, k + ncl, ...
+    cluster_sync();
+    for (int r = split + ncl * (threadIdx.x / TR); r < 16 && r0 + r < npairs; r += ncl * (kWarps * 32 / TR)) {
+      const int col = (threadIdx.x % TR) * 4;
+      float2 ml[8];
+      float4 v[8];
+      float mm = -INFINITY;
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < ncl) {
+          ml[k] = ld_cluster2(mapa_rank(part_ml + r, k));
+          v[k] = ld_cluster4(mapa_rank(part + r * D + col, k));
+          mm = fmaxf(mm, ml[k].x);
+        }
+      const float base = mm == -INFINITY ? 0.f : mm;
+      float ll = 0.f;
+      float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int k = 0; k < 8; ++k)
+        if (k < ncl) {
+          const float f = ex2(ml[k].x - base);
+          ll += f * ml[k].y;
+          acc.x += f * v[k].x;
+          acc.y += f * v[k].y;
+          acc.z += f * v[k].z;
+          acc.w += f * v[k].w;
+        }
+      const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
+      const int i = (r0 + r) / a.group;
+      const int t = t0 + i, h = hk * a.group + (r0 + r) - i * a.group;
+      uint32_t* dst = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + t * a.ldo + h * D + col);
+      *reinterpret_cast<uint2*>(dst) = make_uint2(pack2<BF>(acc.x * inv, acc.y * inv), pack2<BF>(acc.z * inv, acc.w * inv));
+    }
+    cluster_sync();  // no CTA leaves while its part is read
   }
   if (waits) grid_wait();
 }
@@ -445,6 +528,9 @@ __global__ void __launch_bounds__(256) attn_paged_join(const __grid_constant__ P
 // rise past kPartRows, and is at most kPartRows or 2 rows.
 constexpr int kPartRows = 2048;
 constexpr int kMaxSlots = 128;
+// Bytes of the prefix that a small call may read once per sequence instead
+// of once for all.
+constexpr int64_t kReadAgain = 32 << 20;
 static int paged_slots(int rows) { return std::min(kMaxSlots, std::max(2, kPartRows / std::max(1, rows))); }
 
 size_t attn_paged_bytes(const PagedArgs& p, int rows, int heads) {
@@ -474,17 +560,21 @@ static int wide_splits(int64_t items, int64_t blocks, int64_t slots, int64_t row
 // A launch that may start while the kernel before it in the stream runs
 // (grid_wait inside it).
 static cudaError_t launch_early(void (*kernel)(PagedAttnArgs), unsigned grid, unsigned threads, size_t smem,
-                                cudaStream_t s, const PagedAttnArgs& a) {
+                                cudaStream_t s, const PagedAttnArgs& a, unsigned cluster = 1) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = s;
-  cudaLaunchAttribute at[1];
+  cudaLaunchAttribute at[2];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
-  cfg.numAttrs = 1;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
   return cudaLaunchKernelEx(&cfg, kernel, a);
 }
 
@@ -521,12 +611,25 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     e = launch_attn_wide(a, WIDE_JOINT, pair, static_cast<int>(tiles), a.slots, s);
     return e != cudaSuccess || a.slots == 1 ? e : join();
   }
-  // few rows per sequence: the prefix for the rows of all sequences, each
-  // sequence's own keys for its own
   const int R = 16;
-  a.own_tiles = static_cast<int>(pairs / R + seqs);
-  // parts of the few-row tiles: enough CTAs for two waves of three per SM,
-  // none of fewer than 256 keys
+  const int64_t own_tiles = pairs / R + seqs;
+  a.own_tiles = static_cast<int>(own_tiles);
+  // a small call: one launch in which every sequence reads the prefix itself
+  const int64_t again = own_tiles * hk * P * (4 * D);  // bytes of that
+  const int64_t keys = static_cast<int64_t>(P) + a.kv.table_rows;
+  int64_t ncl = std::min<int64_t>(2 * static_cast<int64_t>(sm_count()) / (own_tiles * hk), keys / 128);
+  ncl = ncl >= 8 ? 8 : ncl >= 4 ? 4 : ncl >= 2 ? 2 : 1;
+  if (again <= kReadAgain && keys <= 1024 * ncl && own_tiles * hk * ncl <= 0x7fffffff) {
+    a.cluster = static_cast<int>(ncl);
+    a.own_splits = 1;
+    a.slots = 1;
+    a.first = 1;
+    return launch_early(attn_paged_narrow<BF, D>, static_cast<unsigned>(own_tiles * hk * ncl), kWarps * 32, smem, s, a,
+                        static_cast<unsigned>(ncl));
+  }
+  // few rows per sequence: the prefix for the rows of all sequences, each
+  // sequence's own keys for its own. Parts of the few-row tiles: enough CTAs
+  // for two waves of three per SM, none of fewer than 256 keys
   const int64_t want = 6 * static_cast<int64_t>(sm_count());
   auto splits = [&](int64_t tiles, int64_t keys, int cap, int* part) {
     int64_t n = std::min<int64_t>((want + tiles * hk - 1) / (tiles * hk), (keys + 255) / 256);

@@ -57,6 +57,7 @@ struct PagedAttnArgs {
   int pre_tiles, pre_splits;  // few-row tiles of the prefix, and the parts of its keys
   int own_tiles, own_splits;
   int pre_keys, own_keys;     // keys of a few-row part
+  int cluster;                // > 0: few-row tiles walk [prefix, own keys], split over a cluster
   int first;                  // this kernel is the call's first
   int slots;                  // parts per row; 1: the part is the result
   float* part_o;              // [slots][rows][heads][dim]
