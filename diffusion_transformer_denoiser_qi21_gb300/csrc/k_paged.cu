@@ -539,19 +539,34 @@ size_t attn_paged_bytes(const PagedArgs& p, int rows, int heads) {
   return most * heads * (static_cast<size_t>(p.dim) * 4 + 8) + 256;
 }
 
-// Parts of a wide call's keys: the count that ends first, by a model of one
-// item's time in key blocks (its blocks, and about four of set-up and end)
-// over the waves of items, plus the parts' write and read back at about
-// 6 TB/s against 0.8 us a block.
-static int wide_splits(int64_t items, int64_t blocks, int64_t slots, int64_t rows_heads, int dim, int most) {
-  int best = 1;
+// Parts of a wide call's keys: the count that ends first by a model in
+// microseconds. A CTA takes `fixed` to start and end and `per_block` for each
+// of its key blocks; the few-row tiles that run beside it take `beside`
+// SM-microseconds (their lengths are known to the device alone: half the
+// table's rows is assumed, so a count that makes the wide part itself 1.6
+// times longer than need be is out); parts are written and read back at
+// about 4 TB/s. Fewer parts pay `fixed` less often, more fill the GPU.
+static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block, double beside, int64_t rows_heads,
+                       int dim, int most) {
+  const double fixed = 8.0, sms = sm_count();
   double least = 0.0;
-  for (int n = 1; n <= most && n <= blocks; ++n) {
-    const double t = static_cast<double>((items * n + slots - 1) / slots) * ((blocks + n - 1) / n + 4) +
-                     (n > 1 ? n * static_cast<double>(rows_heads) * dim * 8 / 4.8e6 : 0.0);
-    if (n == 1 || t < least) {
-      best = n;
-      least = t;
+  int best = 1;
+  for (int pass = 0; pass < 2; ++pass) {  // the shortest wide part, then the choice
+    double got = 0.0;
+    for (int n = 1; n <= most && (n == 1 || n <= blocks); ++n) {
+      const double one = static_cast<double>((blocks + n - 1) / n) * per_block + fixed;
+      const double all = static_cast<double>(items) * n * ctas;
+      const double alone = std::ceil(all / sms) * one;
+      if (pass == 0) {
+        if (n == 1 || alone < least) least = alone;
+      } else if (alone <= 1.6 * least) {
+        const double t = std::max(alone, (all * one + beside) / sms) +
+                         (n > 1 || beside > 0 ? n * static_cast<double>(rows_heads) * dim * 8 / 4e6 : 0.0);
+        if (got == 0.0 || t < got) {
+          got = t;
+          best = n;
+        }
+      }
     }
   }
   return best;
@@ -593,6 +608,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   const int most = paged_slots(a.rows);
   const int tokens = a.kv.npages > 0 ? wide_tokens(a.group) : 0;
   cudaError_t e = cudaSuccess;
+  auto block_us = [](bool pair) { return D == 64 ? 0.65 : pair ? 0.8 : 1.3; };  // measured
   auto join = [&] {
     return launch_early(attn_paged_join<BF, D>, static_cast<unsigned>((all + 7) / 8), 256, 0, s, a);
   };
@@ -606,7 +622,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     const int64_t tiles = a.rows / per + seqs;
     const int64_t blocks = (static_cast<int64_t>(P) + 127) / 128 + (static_cast<int64_t>(a.kv.table_rows) + 127) / 128;
     if (tiles > 0x3fffffff / kMaxSlots) return cudaErrorInvalidValue;
-    a.slots = wide_splits(tiles * hk, blocks, sm_count() / (pair ? 2 : 1), all, D, most);
+    a.slots = wide_splits(tiles * hk, pair ? 2 : 1, blocks, block_us(pair), 0.0, all, D, most);
     place_parts();
     e = launch_attn_wide(a, WIDE_JOINT, pair, static_cast<int>(tiles), a.slots, s);
     return e != cudaSuccess || a.slots == 1 ? e : join();
@@ -643,8 +659,9 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   int wide_tiles = 0;
   if (wide) {
     wide_tiles = (a.rows + per - 1) / per;
-    a.pre_splits = wide_splits(static_cast<int64_t>(wide_tiles) * hk, (static_cast<int64_t>(P) + 127) / 128,
-                               sm_count() / (pair ? 2 : 1), all, D, most - 1);
+    const double own_bytes = 0.5 * seqs * a.kv.table_rows * hk * (4.0 * D);
+    a.pre_splits = wide_splits(static_cast<int64_t>(wide_tiles) * hk, pair ? 2 : 1, (static_cast<int64_t>(P) + 127) / 128,
+                               block_us(pair), own_bytes / 30e3, all, D, most - 1);
   } else if (P > 0) {
     a.pre_tiles = static_cast<int>((pairs + R - 1) / R);
     a.pre_splits = splits(a.pre_tiles, P, most - 1, &a.pre_keys);

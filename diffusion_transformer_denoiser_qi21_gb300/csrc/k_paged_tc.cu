@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
   uint32_t* tslot = reinterpret_cast<uint32_t*>(pvdone + kWNS);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tslot + 1);
 
-  if (threadIdx.x == 0) {
+  if (threadIdx.x == 2 * 32) {
     mbar_init(qfull, 1);
     mbar_init(&vtail[0], 1);
     mbar_init(&vtail[1], 1);
@@ -138,14 +138,9 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
       tmem_relinquish();
     }
   }
-  tc_fence_before();
-  if (PAIR)
-    cluster_sync();  // both CTAs' barriers and TMEM ready before any remote use
-  else
-    __syncthreads();
-  tc_fence_after();
-  // what came before the call is done from here on (the set-up above touches
-  // none of it); the call's next kernel may start
+  // what came before the call is done from here on; the call's next kernel
+  // may start. The item is found by every warp while the barriers and the
+  // tensor memory are set up
   grid_wait();
   grid_release();
   // the item: tokens [tok0, tok_end) of this CTA's tile and the keys that its
@@ -195,6 +190,40 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
   const int j1 = static_cast<int>(static_cast<int64_t>(nb) * (split + 1) / p.splits);
   const int n = j1 - j0;
 
+  // the loading warps (below) start on their first page ids here
+  const bool is_k = warp == 0;
+  const int brs = p.br_shift;
+  const int keys = is_k ? W::kKeysK : kWK;              // of a block, in this CTA
+  const int boxes = keys >> brs;                        // per column piece: 1, 2, 4 or 8
+  const int bxs = (is_k && PAIR ? 6 : 7) - brs;         // log2
+  const int run = 32 >> bxs;                            // blocks of a run
+  const int koff = (is_k ? rank * W::kKeysK : 0) + ((lane & (boxes - 1)) << brs);
+  const int none = a.kv.npages * a.kv.page_rows;        // a row behind the pool: zeros
+  // this lane's box of the run from block i on: its key (-1: behind the
+  // end) and its page id
+  int key = -1, id = 0;
+  auto ids = [&](int i) {
+    const int j = j0 + i + (lane >> bxs);
+    const bool pre = j < npb;
+    key = (pre ? j : j - npb) * kWK + koff;
+    if (i + (lane >> bxs) >= n || key >= (pre ? np : no)) key = -1;
+    if (key >= 0) id = __ldg((pre ? a.kv.prefix_pages : own_pages) + key / a.kv.page_rows);
+  };
+  auto row_of = [&]() {
+    if (key < 0) return none;
+    if (id < 0 || id >= a.kv.npages) {
+      atomicOr(&s_wide_status, kStatusPage);
+      return none;
+    }
+    return id * a.kv.page_rows + key % a.kv.page_rows;
+  };
+  if (warp == 0 || warp == 11) ids(0);
+  tc_fence_before();
+  if (PAIR)
+    cluster_sync();  // both CTAs' barriers and TMEM ready before any remote use
+  else
+    __syncthreads();
+  tc_fence_after();
   const uint32_t tmem = *tslot;
   const uint32_t tS = tmem;        // S buffers at columns [0, 384)
   const uint32_t tO = tmem + 384;  // O at columns [384, 384 + D)
@@ -218,7 +247,6 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
     // run's pages are under way meanwhile, and lane 0 issues the boxes: a
     // block must not wait for its page ids, nor K for V's stage
     if (n > 0) {
-      const bool is_k = warp == 0;
       if (is_k && lane == 0) {
         const uint32_t bytes = static_cast<uint32_t>(W::kCols) * p.tokens * a.group * 128;
         if (leader) mbar_arrive_expect_tx(qfull, CT * bytes);
@@ -229,31 +257,6 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
             tma_load_3d(smem + c * 16384, &p.qmap, qfull, c * 64, hk * a.group, tok0);
         }
       }
-      const int brs = p.br_shift;
-      const int keys = is_k ? W::kKeysK : kWK;              // of a block, in this CTA
-      const int boxes = keys >> brs;                        // per column piece: 1, 2, 4 or 8
-      const int bxs = (is_k && PAIR ? 6 : 7) - brs;         // log2
-      const int run = 32 >> bxs;                            // blocks of a run
-      const int koff = (is_k ? rank * W::kKeysK : 0) + ((lane & (boxes - 1)) << brs);
-      const int none = a.kv.npages * a.kv.page_rows;        // a row behind the pool: zeros
-      // this lane's box of the run from block i on: its key (-1: behind the
-      // end) and its page id
-      int key, id;
-      auto ids = [&](int i) {
-        const int j = j0 + i + (lane >> bxs);
-        const bool pre = j < npb;
-        key = (pre ? j : j - npb) * kWK + koff;
-        if (i + (lane >> bxs) >= n || key >= (pre ? np : no)) key = -1;
-        if (key >= 0) id = __ldg((pre ? a.kv.prefix_pages : own_pages) + key / a.kv.page_rows);
-      };
-      auto row_of = [&]() {
-        if (key < 0) return none;
-        if (id < 0 || id >= a.kv.npages) {
-          atomicOr(&s_wide_status, kStatusPage);
-          return none;
-        }
-        return id * a.kv.page_rows + key % a.kv.page_rows;
-      };
       uint64_t* full = is_k ? kfull : vfull;
       uint64_t* empty = is_k ? kempty : vempty;
       const int stage = is_k ? W::kK : W::kV;
@@ -263,7 +266,6 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
       uint8_t* ring = smem + (is_k ? W::kOffK : W::kOffV);
       bool ok = true;
       int rows = none, tails = 0;
-      ids(0);
       for (int i = 0; i < n && ok; ++i) {
         if ((i & (run - 1)) == 0) {
           rows = row_of();
