@@ -84,7 +84,7 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 }
 
 // ------------------------------------------------------- few rows a tile --
-// A CTA takes a tile of 16 (row, head) pairs of one key head and a part of
+// A CTA takes a tile of 16 MT (row, head) pairs of one key head and a part of
 // the keys, the prefix's or a sequence's own. Its four warps take granules
 // of 16 keys in turn, each through a ring of its own (16-byte asynchronous
 // copies, rows behind the end filled with zeros), so no warp waits for
@@ -101,18 +101,24 @@ __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], 
 template <int D>
 constexpr int kNarrowStages = D == 128 ? 2 : 3;
 template <int D>
-constexpr int kNarrowRing = kWarps * kNarrowStages<D> * 2 * kGran * D * 2;
-template <int D>
-constexpr int kNarrowSmem = kNarrowRing<D> + 16 * (D * 4 + 8);  // a CTA's part: sums, then (max, sum)
+constexpr int kNarrowRing = kNarrowStages<D> * 2 * kGran * D * 2;  // of a warp
+// The warps' f32 sums take the rings' place at the end, where they need more.
+template <int D, int MT>
+constexpr int kNarrowSums = 16 * MT * (D + 4) * 4 > kNarrowRing<D> ? 16 * MT * (D + 4) * 4 : kNarrowRing<D>;
+template <int D, int MT>
+constexpr int kNarrowPart = kWarps * kNarrowSums<D, MT>;  // offset of a CTA's part: sums, then (max, sum)
+template <int D, int MT>
+constexpr int kNarrowSmem = kNarrowPart<D, MT> + 16 * MT * (D * 4 + 8);
 
-template <bool BF, int D>
+template <bool BF, int D, int MT>
 __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_constant__ PagedAttnArgs a) {
+  constexpr int R = 16 * MT;
   constexpr int NST = kNarrowStages<D>;
   constexpr int HALF = kGran * D * 2;  // bytes of a granule's K (or V)
   constexpr int CH = D / 8;            // 16-byte pieces of a row
   constexpr int RS = 32 / CH;          // rows that a warp copies at once
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float s_m[kWarps][16], s_l[kWarps][16];
+  __shared__ float s_m[kWarps][R], s_l[kWarps][R];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   // the key heads of a tile run side by side: their rows share DRAM pages
   const int ncl = max(1, a.cluster);
@@ -138,17 +144,17 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     split = x - tile * a.pre_splits;
     slot = split;
     npairs = min(max(__ldg(a.kv.cu + a.kv.nseq), 0), a.rows) * a.group;
-    r0 = tile * 16;
+    r0 = tile * R;
   } else {
     x -= a.pre_tiles * a.pre_splits;
     const int tile = x / a.own_splits;
     split = a.cluster ? static_cast<int>(cluster_rank()) : x - tile * a.own_splits;
     slot = a.pre_splits + split;
-    const SeqTile q = warp_find_tile(a, tile, a.group, 16, lane);
+    const SeqTile q = warp_find_tile(a, tile, a.group, R, lane);
     t0 = q.row0;
     nrows = q.rows;
     npairs = nrows * a.group;  // 0 if there is no such tile
-    r0 = q.at * 16;
+    r0 = q.at * R;
     own_pages = a.kv.table + static_cast<int64_t>(q.b) * a.kv.table_stride;
     len = q.len;
     if (npairs > 0 && (len < nrows || len > a.kv.table_rows) && threadIdx.x == 0) atomicOr(&s_paged_status, kStatusPage);
@@ -159,15 +165,16 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     return;
   }
 
-  // this thread's rows: lane / 4 and + 8; the keys that they see of the
+  // this thread's rows: lane / 4 and + 8 of every 16; the keys that they see of the
   // prefix and of the own ones, and the most and least of the tile
   const int tq = lane >> 2, tj = lane & 3;
-  int lim_p[2], lim_o[2];
-  uint32_t qf[D / 16][4];
+  int lim_p[MT][2], lim_o[MT][2];
+  uint32_t qf[MT][D / 16][4];
   int most_p = 0, most_o = 0, least_p = 0x7fffffff, least_o = 0x7fffffff;
 #pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    const int pr = r0 + tq + 8 * e;
+  for (int me = 0; me < 2 * MT; ++me) {
+    const int mt = me >> 1, e = me & 1;
+    const int pr = r0 + 16 * mt + tq + 8 * e;
     const bool live = pr < npairs;
     const int i = live ? pr / a.group : 0;
     const int t = t0 + i;
@@ -177,20 +184,20 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
       n = static_cast<int>(min(__ldg(a.vis + t), static_cast<uint32_t>(n)));
     else if (a.causal && !pre)
       n = P + min(max(len - nrows + i + 1, 0), len);
-    lim_p[e] = live ? min(n, np) : 0;
-    lim_o[e] = live ? min(max(n - P, 0), len) : 0;
-    most_p = max(most_p, lim_p[e]);
-    most_o = max(most_o, lim_o[e]);
+    lim_p[mt][e] = live ? min(n, np) : 0;
+    lim_o[mt][e] = live ? min(max(n - P, 0), len) : 0;
+    most_p = max(most_p, lim_p[mt][e]);
+    most_o = max(most_o, lim_o[mt][e]);
     if (live) {
-      least_p = min(least_p, lim_p[e]);
-      least_o = min(least_o, lim_o[e]);
+      least_p = min(least_p, lim_p[mt][e]);
+      least_o = min(least_o, lim_o[mt][e]);
     }
     const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
                                                            static_cast<int64_t>(t) * a.ldq + h * D);
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
-      qf[k][e] = live ? __ldg(qr + 8 * k + tj) : 0u;
-      qf[k][2 + e] = live ? __ldg(qr + 8 * k + 4 + tj) : 0u;
+      qf[mt][k][e] = live ? __ldg(qr + 8 * k + tj) : 0u;
+      qf[mt][k][2 + e] = live ? __ldg(qr + 8 * k + 4 + tj) : 0u;
     }
   }
   most_p = __reduce_max_sync(0xffffffffu, most_p);
@@ -252,12 +259,16 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     }
   };
 
-  float o[D / 8][4];
+  float o[MT][D / 8][4], m[MT][2], l[MT][2];
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n)
+  for (int mt = 0; mt < MT; ++mt) {
 #pragma unroll
-    for (int e = 0; e < 4; ++e) o[n][e] = 0.f;
-  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+    for (int n = 0; n < D / 8; ++n)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) o[mt][n][e] = 0.f;
+    m[mt][0] = m[mt][1] = -INFINITY;
+    l[mt][0] = l[mt][1] = 0.f;
+  }
 
   int nf = g0;  // next granule to fetch
   int nid = nf < g1 ? page_of(nf) : 0;
@@ -290,100 +301,121 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     const uint32_t sk = sring + st * 2 * HALF + kkey * (D * 2), sv = sring + st * 2 * HALF + HALF + vkey * (D * 2);
     if (++st == NST) st = 0;
 
-    float s[2][4];
+    float s[MT][2][4];
 #pragma unroll
-    for (int n = 0; n < 2; ++n)
+    for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int e = 0; e < 4; ++e) s[n][e] = 0.f;
+      for (int n = 0; n < 2; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[mt][n][e] = 0.f;
 #pragma unroll
     for (int k = 0; k < D / 16; ++k) {
       uint32_t b[4];
       ldsm4<false>(sk + (kx ^ (k << 5)), b);
-      mma16816<BF>(s[0], qf[k], b[0], b[1]);
-      mma16816<BF>(s[1], qf[k], b[2], b[3]);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mma16816<BF>(s[mt][0], qf[mt][k], b[0], b[1]);
+        mma16816<BF>(s[mt][1], qf[mt][k], b[2], b[3]);
+      }
     }
     const bool of_p = g < gp;
     const int key = (of_p ? g : g - gp) * kGran;
     if (key + kGran > (of_p ? least_p : least_o)) {  // what a row does not see is taken out
-      const int lim[2] = {of_p ? lim_p[0] : lim_o[0], of_p ? lim_p[1] : lim_o[1]};
       const int col = key + 2 * tj;
 #pragma unroll
-      for (int n = 0; n < 2; ++n)
+      for (int mt = 0; mt < MT; ++mt) {
+        const int lim[2] = {of_p ? lim_p[mt][0] : lim_o[mt][0], of_p ? lim_p[mt][1] : lim_o[mt][1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (col + 8 * n + (e & 1) >= lim[e >> 1]) s[n][e] = -INFINITY;
-    }
-    uint32_t p[4];
-    float al[2];
-    bool moved = false;
+        for (int n = 0; n < 2; ++n)
 #pragma unroll
-    for (int e = 0; e < 2; ++e) {
-      float mx = fmaxf(fmaxf(s[0][2 * e], s[0][2 * e + 1]), fmaxf(s[1][2 * e], s[1][2 * e + 1]));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-      mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * c;
-      // the maximum (log2 units) is raised only past the threshold: o and l
-      // share it
-      al[e] = 1.f;
-      if (mx > m[e] + kPagedRescale) {
-        al[e] = ex2(m[e] - mx);
-        m[e] = mx;
-        moved = true;
+          for (int e = 0; e < 4; ++e)
+            if (col + 8 * n + (e & 1) >= lim[e >> 1]) s[mt][n][e] = -INFINITY;
       }
-      // a row that has seen no key yet has weights 2^(-inf - 0) = 0
-      const float base = m[e] == -INFINITY ? 0.f : -m[e];
-      const float p0 = ex2(fmaf(s[0][2 * e], c, base)), p1 = ex2(fmaf(s[0][2 * e + 1], c, base));
-      const float p2 = ex2(fmaf(s[1][2 * e], c, base)), p3 = ex2(fmaf(s[1][2 * e + 1], c, base));
-      // P is rounded to the values' type for the MMA (half a step of a
-      // weight each, of either sign); l sums the f32 weights
-      p[e] = pack2<BF>(p0, p1);
-      p[2 + e] = pack2<BF>(p2, p3);
-      l[e] = fmaf(l[e], al[e], (p0 + p1) + (p2 + p3));
     }
-    if (__any_sync(0xffffffffu, moved)) {
+    uint32_t p[MT][4];
 #pragma unroll
-      for (int n = 0; n < D / 8; ++n) {
-        o[n][0] *= al[0];
-        o[n][1] *= al[0];
-        o[n][2] *= al[1];
-        o[n][3] *= al[1];
+    for (int mt = 0; mt < MT; ++mt) {
+      float al[2];
+      bool moved = false;
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const float s0 = s[mt][0][2 * e], s1 = s[mt][0][2 * e + 1], s2 = s[mt][1][2 * e], s3 = s[mt][1][2 * e + 1];
+        float mx = fmaxf(fmaxf(s0, s1), fmaxf(s2, s3));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2)) * c;
+        // the maximum (log2 units) is raised only past the threshold: o and l
+        // share it
+        al[e] = 1.f;
+        if (mx > m[mt][e] + kPagedRescale) {
+          al[e] = ex2(m[mt][e] - mx);
+          m[mt][e] = mx;
+          moved = true;
+        }
+        // a row that has seen no key yet has weights 2^(-inf - 0) = 0
+        const float base = m[mt][e] == -INFINITY ? 0.f : -m[mt][e];
+        const float p0 = ex2(fmaf(s0, c, base)), p1 = ex2(fmaf(s1, c, base));
+        const float p2 = ex2(fmaf(s2, c, base)), p3 = ex2(fmaf(s3, c, base));
+        // P is rounded to the values' type for the MMA (half a step of a
+        // weight each, of either sign); l sums the f32 weights
+        p[mt][e] = pack2<BF>(p0, p1);
+        p[mt][2 + e] = pack2<BF>(p2, p3);
+        l[mt][e] = fmaf(l[mt][e], al[e], (p0 + p1) + (p2 + p3));
+      }
+      if (__any_sync(0xffffffffu, moved)) {
+#pragma unroll
+        for (int n = 0; n < D / 8; ++n) {
+          o[mt][n][0] *= al[0];
+          o[mt][n][1] *= al[0];
+          o[mt][n][2] *= al[1];
+          o[mt][n][3] *= al[1];
+        }
       }
     }
 #pragma unroll
     for (int n = 0; n < D / 16; ++n) {
       uint32_t b[4];
       ldsm4<true>(sv + (vx ^ (n << 5)), b);
-      mma16816<BF>(o[2 * n], p, b[0], b[1]);
-      mma16816<BF>(o[2 * n + 1], p, b[2], b[3]);
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt) {
+        mma16816<BF>(o[mt][2 * n], p[mt], b[0], b[1]);
+        mma16816<BF>(o[mt][2 * n + 1], p[mt], b[2], b[3]);
+      }
     }
     __syncwarp();  // the stage is refilled next round
   }
   cp_async_wait<0>();
 
   // join the four warps: each leaves its sums in its ring
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    float sum = l[e];
-    sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-    sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-    if (tj == 0) {
-      s_m[warp][tq + 8 * e] = m[e];
-      s_l[warp][tq + 8 * e] = sum;
-    }
-  }
   constexpr int OP = D + 4;  // row pitch of the f32 sums: spreads the rows over the banks
-  static_assert(16 * OP * 4 <= NST * 2 * HALF, "the sums fit the ring");
-  float* so = reinterpret_cast<float*>(smem + warp * (NST * 2 * HALF));
-  __syncwarp();
+  float* so = reinterpret_cast<float*>(smem + warp * kNarrowSums<D, MT>);
+  if (kNarrowSums<D, MT> > kNarrowRing<D>)
+    __syncthreads();  // they reach into another warp's ring
+  else
+    __syncwarp();
 #pragma unroll
-  for (int n = 0; n < D / 8; ++n) {
-    *reinterpret_cast<float2*>(so + tq * OP + 8 * n + 2 * tj) = make_float2(o[n][0], o[n][1]);
-    *reinterpret_cast<float2*>(so + (tq + 8) * OP + 8 * n + 2 * tj) = make_float2(o[n][2], o[n][3]);
+  for (int mt = 0; mt < MT; ++mt) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float sum = l[mt][e];
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+      if (tj == 0) {
+        s_m[warp][16 * mt + tq + 8 * e] = m[mt][e];
+        s_l[warp][16 * mt + tq + 8 * e] = sum;
+      }
+    }
+    float* row = so + (16 * mt + tq) * OP + 2 * tj;
+#pragma unroll
+    for (int n = 0; n < D / 8; ++n) {
+      *reinterpret_cast<float2*>(row + 8 * n) = make_float2(o[mt][n][0], o[mt][n][1]);
+      *reinterpret_cast<float2*>(row + 8 * OP + 8 * n) = make_float2(o[mt][n][2], o[mt][n][3]);
+    }
   }
   __syncthreads();
   constexpr int TR = D / 4;  // threads of a row, 4 values each
-  float* part = reinterpret_cast<float*>(smem + kNarrowRing<D>);
-  float2* part_ml = reinterpret_cast<float2*>(part + 16 * D);
-  for (int r = threadIdx.x / TR; r < 16; r += kWarps * 32 / TR) {
+  float* part = reinterpret_cast<float*>(smem + kNarrowPart<D, MT>);
+  float2* part_ml = reinterpret_cast<float2*>(part + R * D);
+  for (int r = threadIdx.x / TR; r < R; r += kWarps * 32 / TR) {
     const int pr = r0 + r;
     if (pr >= npairs) break;
     const int col = (threadIdx.x % TR) * 4;
@@ -397,7 +429,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     for (int w = 0; w < kWarps; ++w) {
       const float f = ex2(s_m[w][r] - base);
       const float4 v = *reinterpret_cast<const float4*>(
-          reinterpret_cast<const float*>(smem + w * (NST * 2 * HALF)) + r * OP + col);
+          reinterpret_cast<const float*>(smem + w * kNarrowSums<D, MT>) + r * OP + col);
       ll += f * s_l[w][r];
       acc.x += f * v.x;
       acc.y += f * v.y;
@@ -424,7 +456,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
   if (ncl > 1) {
     // the cluster's parts: CTA k finishes rows k, k + ncl, ...
     cluster_sync();
-    for (int r = split + ncl * (threadIdx.x / TR); r < 16 && r0 + r < npairs; r += ncl * (kWarps * 32 / TR)) {
+    for (int r = split + ncl * (threadIdx.x / TR); r < R && r0 + r < npairs; r += ncl * (kWarps * 32 / TR)) {
       const int col = (threadIdx.x % TR) * 4;
       float2 ml[8];
       float4 v[8];
@@ -461,58 +493,78 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
 }
 
 // ----------------------------------------------------------------- join --
-// One warp per (row, head): weights 2^(m_s - m) of the slots, then the
-// weighted sum of their f32 parts over the joined sum. Bound by reading the
-// parts, which the L2 still holds.
+// The parts of one (row, head): weights 2^(m_s - m) of the slots, then the
+// weighted sum of their f32 parts over the joined sum. `warps` warps of a CTA
+// take the slots of a pair in turn, eight loads at a time (a lone row split
+// over a hundred parts would else wait for them one after the other), and
+// meet in shared memory. Bound by reading the parts, which the L2 still
+// holds.
 template <bool BF, int D>
-__global__ void __launch_bounds__(256) attn_paged_join(const __grid_constant__ PagedAttnArgs a) {
-  const int lane = threadIdx.x & 31;
-  const int64_t pair = static_cast<int64_t>(blockIdx.x) * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(256) attn_paged_join(const __grid_constant__ PagedAttnArgs a, int warps) {
+  constexpr int V = D / 32;
+  __shared__ __align__(16) float s_acc[8][D];
+  __shared__ float2 s_ml[8];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int w = warp % warps;
+  const int64_t pair = static_cast<int64_t>(blockIdx.x) * (8 / warps) + warp / warps;
   grid_wait();
   const int64_t pairs = static_cast<int64_t>(min(max(__ldg(a.kv.cu + a.kv.nseq), 0), a.rows)) * a.heads;
-  if (pair >= pairs) return;
   const int64_t step = static_cast<int64_t>(a.rows) * a.heads;
-  float mm = -INFINITY;
-  for (int s = lane; s < a.slots; s += 32) mm = fmaxf(mm, a.part_ml[s * step + pair].x);
+  const bool live = pair < pairs;
+  // this warp's slots: w, w + warps, ..., at most 16 (128 slots, 8 warps)
+  const int mine = live ? (a.slots - w + warps - 1) / warps : 0;
+  float2 ml = make_float2(-INFINITY, 0.f);
+  if (lane < mine) ml = a.part_ml[(w + lane * warps) * step + pair];
+  float mm = ml.x;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) mm = fmaxf(mm, __shfl_xor_sync(0xffffffffu, mm, o));
-  const float base = mm == -INFINITY ? 0.f : mm;
-  constexpr int V = D / 32;
-  float acc[V] = {};
-  float ll = 0.f;
-  for (int s0 = 0; s0 < a.slots; s0 += 32) {
-    float w = 0.f;
-    if (s0 + lane < a.slots) {
-      const float2 ml = a.part_ml[(s0 + lane) * step + pair];
-      w = ex2(ml.x - base);
-      ll += w * ml.y;
-    }
-    const int n = min(32, a.slots - s0);
-    for (int s = 0; s < n; s += 8) {
-      float ws[8];
-      alignas(16) float v[8][V];
-#pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        ws[k] = __shfl_sync(0xffffffffu, w, (s + k) & 31);
-        if (s + k >= n) ws[k] = 0.f;
-#pragma unroll
-        for (int i = 0; i < V; ++i) v[k][i] = 0.f;
-        if (ws[k] != 0.f) {  // a part without keys may hold no sums
-          const float* src = a.part_o + ((s0 + s + k) * step + pair) * D + lane * V;
-          if constexpr (V == 4)
-            *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
-          else
-            *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < 8; ++k)
-#pragma unroll
-        for (int i = 0; i < V; ++i) acc[i] += ws[k] * v[k][i];
-    }
-  }
+  const float wt = ex2(ml.x - (mm == -INFINITY ? 0.f : mm));
+  float ll = lane < mine ? wt * ml.y : 0.f;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) ll += __shfl_xor_sync(0xffffffffu, ll, o);
+  float acc[V] = {};
+  for (int s = 0; s < mine; s += 8) {
+    float ws[8];
+    alignas(16) float v[8][V];
+#pragma unroll
+    for (int k = 0; k < 8; ++k) {
+      ws[k] = __shfl_sync(0xffffffffu, wt, (s + k) & 31);
+      if (s + k >= mine) ws[k] = 0.f;
+#pragma unroll
+      for (int i = 0; i < V; ++i) v[k][i] = 0.f;
+      if (ws[k] != 0.f) {  // a part without keys may hold no sums
+        const float* src = a.part_o + ((w + (s + k) * warps) * step + pair) * D + lane * V;
+        if constexpr (V == 4)
+          *reinterpret_cast<float4*>(v[k]) = *reinterpret_cast<const float4*>(src);
+        else
+          *reinterpret_cast<float2*>(v[k]) = *reinterpret_cast<const float2*>(src);
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 8; ++k)
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += ws[k] * v[k][i];
+  }
+  if (warps > 1) {
+    if (lane == 0) s_ml[warp] = make_float2(mm, ll);
+#pragma unroll
+    for (int i = 0; i < V; ++i) s_acc[warp][lane * V + i] = acc[i];
+    __syncthreads();
+    if (w != 0) return;
+    for (int k = 0; k < warps; ++k) mm = fmaxf(mm, s_ml[warp + k].x);
+    const float base = mm == -INFINITY ? 0.f : mm;
+    ll = 0.f;
+#pragma unroll
+    for (int i = 0; i < V; ++i) acc[i] = 0.f;
+    for (int k = 0; k < warps; ++k) {
+      const float f = ex2(s_ml[warp + k].x - base);
+      if (f == 0.f) continue;
+      ll += f * s_ml[warp + k].y;
+#pragma unroll
+      for (int i = 0; i < V; ++i) acc[i] += f * s_acc[warp + k][lane * V + i];
+    }
+  }
+  if (!live) return;
   const float inv = ll > 0.f || ll != ll ? 1.f / ll : 0.f;
   const int64_t t = pair / a.heads;
   const int h = static_cast<int>(pair - t * a.heads);
@@ -574,8 +626,9 @@ static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block
 
 // A launch that may start while the kernel before it in the stream runs
 // (grid_wait inside it).
-static cudaError_t launch_early(void (*kernel)(PagedAttnArgs), unsigned grid, unsigned threads, size_t smem,
-                                cudaStream_t s, const PagedAttnArgs& a, unsigned cluster = 1) {
+template <class... A>
+static cudaError_t launch_early(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                                unsigned cluster, const A&... args) {
   cudaLaunchConfig_t cfg{};
   cfg.gridDim = dim3(grid);
   cfg.blockDim = dim3(threads);
@@ -590,18 +643,23 @@ static cudaError_t launch_early(void (*kernel)(PagedAttnArgs), unsigned grid, un
   at[1].val.clusterDim.z = 1;
   cfg.attrs = at;
   cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, a);
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
+template <bool BF, int D, int MT>
+static cudaError_t launch_narrow(const PagedAttnArgs& a, unsigned grid, unsigned cluster, cudaStream_t s) {
+  constexpr int smem = kNarrowSmem<D, MT>;
+  static PerDevice<cudaError_t> once;
+  const cudaError_t* attr = once.get([] {
+    return cudaFuncSetAttribute(attn_paged_narrow<BF, D, MT>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  });
+  if (attr == nullptr) return cudaErrorNoDevice;
+  if (*attr != cudaSuccess) return *attr;
+  return launch_early(attn_paged_narrow<BF, D, MT>, grid, kWarps * 32, smem, s, cluster, a);
 }
 
 template <bool BF, int D>
 static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
-  constexpr int smem = kNarrowSmem<D>;
-  static PerDevice<cudaError_t> once;
-  const cudaError_t* attr = once.get([] {
-    return cudaFuncSetAttribute(attn_paged_narrow<BF, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-  });
-  if (attr == nullptr) return cudaErrorNoDevice;
-  if (*attr != cudaSuccess) return *attr;
   const int hk = a.kv.kv_heads, P = a.kv.prefix_len;
   const int64_t pairs = static_cast<int64_t>(a.rows) * a.group, all = static_cast<int64_t>(a.rows) * a.heads;
   const int seqs = std::min(a.kv.nseq, a.rows);
@@ -610,7 +668,8 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   cudaError_t e = cudaSuccess;
   auto block_us = [](bool pair) { return D == 64 ? 0.65 : pair ? 0.8 : 1.3; };  // measured
   auto join = [&] {
-    return launch_early(attn_paged_join<BF, D>, static_cast<unsigned>((all + 7) / 8), 256, 0, s, a);
+    const int warps = a.slots > 32 ? 8 : a.slots > 16 ? 4 : a.slots > 8 ? 2 : 1;
+    return launch_early(attn_paged_join<BF, D>, static_cast<unsigned>((all * warps + 7) / 8), 256, 0, s, 1, a, warps);
   };
   auto place_parts = [&] {
     a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.slots) * a.rows * a.heads * D);
@@ -627,7 +686,16 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     e = launch_attn_wide(a, WIDE_JOINT, pair, static_cast<int>(tiles), a.slots, s);
     return e != cudaSuccess || a.slots == 1 ? e : join();
   }
-  const int R = 16;
+  // tiles of 16 rows, or of 32 where a sequence has more and there are tiles
+  // enough for all SMs (its keys are then copied into shared memory half as
+  // often: 64 sequences of 5 x 4 rows, 500 keys: 38 us against 44; with few
+  // tiles the longer ones only take longer: 16 of 5 x 7 rows: 25 against 23)
+  const bool two = pairs > 16 * static_cast<int64_t>(seqs) && (pairs / 32 + seqs) * hk >= 3 * static_cast<int64_t>(sm_count());
+  const int R = two ? 32 : 16;
+  auto narrow = [&](int64_t grid, int64_t cluster) {
+    const unsigned g = static_cast<unsigned>(grid), c = static_cast<unsigned>(cluster);
+    return two ? launch_narrow<BF, D, 2>(a, g, c, s) : launch_narrow<BF, D, 1>(a, g, c, s);
+  };
   const int64_t own_tiles = pairs / R + seqs;
   a.own_tiles = static_cast<int>(own_tiles);
   // a small call: one launch in which every sequence reads the prefix itself
@@ -640,8 +708,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     a.own_splits = 1;
     a.slots = 1;
     a.first = 1;
-    return launch_early(attn_paged_narrow<BF, D>, static_cast<unsigned>(own_tiles * hk * ncl), kWarps * 32, smem, s, a,
-                        static_cast<unsigned>(ncl));
+    return narrow(own_tiles * hk * ncl, ncl);
   }
   // few rows per sequence: the prefix for the rows of all sequences, each
   // sequence's own keys for its own. Parts of the few-row tiles: enough CTAs
@@ -674,7 +741,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
                            static_cast<int64_t>(a.own_tiles) * a.own_splits);
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
   a.first = !wide;
-  e = launch_early(attn_paged_narrow<BF, D>, static_cast<unsigned>(gx), kWarps * 32, smem, s, a);
+  e = narrow(gx, 1);
   return e != cudaSuccess || a.slots == 1 ? e : join();
 }
 
