@@ -66,6 +66,24 @@ __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
                  : "memory");
 }
 
+__device__ __forceinline__ uint32_t lds32(uint32_t addr) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(addr) : "memory");
+  return v;
+}
+
+// Is a value of the 16 x D granule at `addr` not finite? By one whole warp.
+template <bool BF, int D>
+__device__ __forceinline__ bool odd_granule(uint32_t addr, int lane) {
+  float odd = 0.f;  // NaN once one is met
+#pragma unroll
+  for (int i = 0; i < kGran * D * 2 / 128; ++i) {
+    const float2 v = unpack2<BF>(lds32(addr + i * 128 + lane * 4));
+    odd = fmaf(0.f, v.x, fmaf(0.f, v.y, odd));
+  }
+  return __any_sync(0xffffffffu, odd != odd);
+}
+
 // c += a b, m16n8k16, f32 sums.
 template <bool BF>
 __device__ __forceinline__ void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -298,6 +316,7 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
       if (fs >= NST) fs -= NST;
       fetch_next(fs);
     }
+    const int cur = st;
     const uint32_t sk = sring + st * 2 * HALF + kkey * (D * 2), sv = sring + st * 2 * HALF + HALF + vkey * (D * 2);
     if (++st == NST) st = 0;
 
@@ -320,7 +339,8 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     }
     const bool of_p = g < gp;
     const int key = (of_p ? g : g - gp) * kGran;
-    if (key + kGran > (of_p ? least_p : least_o)) {  // what a row does not see is taken out
+    const bool partly = key + kGran > (of_p ? least_p : least_o);
+    if (partly) {  // what a row does not see is taken out
       const int col = key + 2 * tj;
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt) {
@@ -371,14 +391,41 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
         }
       }
     }
+    const uint32_t sgv = sring + cur * 2 * HALF + HALF;  // the granule's V
+    if (partly && odd_granule<BF, D>(sgv, lane)) {
+      // a weight of 0 does not take out a value that is not finite (0 times
+      // it is a NaN): this granule's sums key by key, over what a row sees
+#pragma unroll 1
+      for (int k = 0; k < kGran; ++k) {
+        const int from = (lane & ~3) | ((k & 7) >> 1);
+        const uint32_t vr = sgv + k * (D * 2) + tj * 4;
 #pragma unroll
-    for (int n = 0; n < D / 16; ++n) {
-      uint32_t b[4];
-      ldsm4<true>(sv + (vx ^ (n << 5)), b);
+        for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-      for (int mt = 0; mt < MT; ++mt) {
-        mma16816<BF>(o[mt][2 * n], p[mt], b[0], b[1]);
-        mma16816<BF>(o[mt][2 * n + 1], p[mt], b[2], b[3]);
+          for (int e = 0; e < 2; ++e) {
+            const uint32_t lo = __shfl_sync(0xffffffffu, p[mt][e], from), hi = __shfl_sync(0xffffffffu, p[mt][2 + e], from);
+            const float2 pp = unpack2<BF>(k < 8 ? lo : hi);
+            const float pk = k & 1 ? pp.y : pp.x;
+            if (key + k < (of_p ? lim_p[mt][e] : lim_o[mt][e])) {
+#pragma unroll
+              for (int n = 0; n < D / 8; ++n) {
+                const float2 v = unpack2<BF>(lds32(vr + ((n ^ (k & 7)) << 4)));
+                o[mt][n][2 * e] = fmaf(pk, v.x, o[mt][n][2 * e]);
+                o[mt][n][2 * e + 1] = fmaf(pk, v.y, o[mt][n][2 * e + 1]);
+              }
+            }
+          }
+      }
+    } else {
+#pragma unroll
+      for (int n = 0; n < D / 16; ++n) {
+        uint32_t b[4];
+        ldsm4<true>(sv + (vx ^ (n << 5)), b);
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt) {
+          mma16816<BF>(o[mt][2 * n], p[mt], b[0], b[1]);
+          mma16816<BF>(o[mt][2 * n + 1], p[mt], b[2], b[3]);
+        }
       }
     }
     __syncwarp();  // the stage is refilled next round

@@ -173,13 +173,18 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
     return n;
   };
   const int item_end = min(tok_end, tok0 + CT * p.tokens);
-  int most = 0;
+  int most = 0, least = 0;
   if (a.vis) {
-    for (int t = tok0 + lane; t < item_end; t += 32) most = max(most, limit(t));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) most = max(most, __shfl_xor_sync(0xffffffffu, most, o));
+    least = 0x7fffffff;
+    for (int t = tok0 + lane; t < item_end; t += 32) {
+      most = max(most, limit(t));
+      least = min(least, limit(t));
+    }
+    most = __reduce_max_sync(0xffffffffu, most);
+    least = __reduce_min_sync(0xffffffffu, least);
   } else if (tok0 < item_end) {
     most = limit(item_end - 1);
+    least = limit(tok0);
   }
   tok0 += rank * p.tokens;
   // key blocks: the prefix's, then the own keys'; this split's are [j0, j1)
@@ -547,6 +552,7 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
     if (ok && !dead) {
       tc_fence_after();
       const int h0 = hk * a.group + r0 - i0 * a.group, h1 = hk * a.group + r1 - i1 * a.group;
+      float odd0 = 0.f, odd1 = 0.f;  // NaN once a sum is not finite
       if (a.slots == 1) {
         const float inv0 = l0 > 0.f || l0 != l0 ? 1.f / l0 : 0.f;  // a row that sees no key is 0
         const float inv1 = l1 > 0.f || l1 != l1 ? 1.f / l1 : 0.f;
@@ -565,6 +571,8 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
 #pragma unroll
           for (int g = 0; g < 8; ++g) {
             const int col = hf * 64 + 8 * g + 2 * tj;
+            odd0 = fmaf(0.f, __uint_as_float(o[4 * g + 0]) + __uint_as_float(o[4 * g + 1]), odd0);
+            odd1 = fmaf(0.f, __uint_as_float(o[4 * g + 2]) + __uint_as_float(o[4 * g + 3]), odd1);
             if (live0)
               *reinterpret_cast<uint32_t*>(o0 + col) =
                   pack2<BF>(__uint_as_float(o[4 * g + 0]) * inv0, __uint_as_float(o[4 * g + 1]) * inv0);
@@ -587,6 +595,8 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
 #pragma unroll
             for (int g = 0; g < 8; ++g) {
               const int col = hf * 64 + 8 * g + 2 * tj;
+              odd0 = fmaf(0.f, __uint_as_float(o[4 * g + 0]) + __uint_as_float(o[4 * g + 1]), odd0);
+              odd1 = fmaf(0.f, __uint_as_float(o[4 * g + 2]) + __uint_as_float(o[4 * g + 3]), odd1);
               if (live0)
                 *reinterpret_cast<uint2*>(a.part_o + at0 * D + col) = make_uint2(o[4 * g + 0], o[4 * g + 1]);
               if (live1)
@@ -594,6 +604,37 @@ __global__ void __launch_bounds__(kWThreads, 1) attn_paged_wide(const __grid_con
             }
           }
         }
+      }
+      // A key that some rows of the tile see and others do not has weight 0 in
+      // those, but 0 times a value that is not finite is a NaN. Rows with such
+      // a sum are done again over the keys that they see alone, if one of the
+      // keys between the tile's limits has such a value
+      const bool fix0 = live0 && odd0 != odd0 && least < most, fix1 = live1 && odd1 != odd1 && least < most;
+      if (__any_sync(0xffffffffu, fix0 || fix1) && n > 0 &&
+          odd_values<BF, D>(a, own_pages, hk, least, most, lane)) {
+        __syncwarp();  // after the stores above, some of which are replaced
+        const int k0 = j0 < npb ? j0 * kWK : P + (j0 - npb) * kWK;             // this split's keys
+        const int k1 = j1 <= npb ? min(j1 * kWK, np) : P + min((j1 - npb) * kWK, no);
+        for (int e = 0; e < 2; ++e)
+          for (unsigned left = __ballot_sync(0xffffffffu, e ? fix1 : fix0); left;) {
+            const int l = __ffs(left) - 1;  // a lane of the row's four
+            left &= ~(0xfu << (l & ~3));
+            const int t = __shfl_sync(0xffffffffu, e ? t1 : t0, l), h = __shfl_sync(0xffffffffu, e ? h1 : h0, l);
+            const float mx = __shfl_sync(0xffffffffu, e ? m1 : m0, l), sum = __shfl_sync(0xffffffffu, e ? l1 : l0, l);
+            float v[D / 32];
+            redo_row<BF, D>(a, own_pages, hk, t, h, k0, min(k1, __shfl_sync(0xffffffffu, e ? lim1 : lim0, l)), mx, lane, v);
+            if (a.slots == 1) {
+              uint16_t* dst = static_cast<uint16_t*>(a.out) + static_cast<int64_t>(t) * a.ldo + h * D + lane * (D / 32);
+              const float inv = sum > 0.f || sum != sum ? 1.f / sum : 0.f;
+#pragma unroll
+              for (int i = 0; i < D / 32; i += 2)
+                *reinterpret_cast<uint32_t*>(dst + i) = pack2<BF>(v[i] * inv, v[i + 1] * inv);
+            } else {
+              float* dst = a.part_o + ((static_cast<int64_t>(split) * a.rows + t) * a.heads + h) * D + lane * (D / 32);
+#pragma unroll
+              for (int i = 0; i < D / 32; ++i) dst[i] = v[i];
+            }
+          }
       }
     }
   }

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "internal.h"
+#include "ptx.cuh"
 
 namespace qi21 {
 
@@ -111,6 +112,75 @@ __device__ __forceinline__ SeqTile warp_find_tile(const PagedAttnArgs& a, int x,
 // its writes are visible; grid_release lets the next one start.
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
+// Key `k` of [prefix, own rows] of a sequence: its K row of key head hk (the
+// V row is kv_heads * D further), or null for a page outside the cache.
+template <int D>
+__device__ __forceinline__ const uint16_t* key_row(const PagedAttnArgs& a, const int32_t* own_pages, int hk, int k) {
+  const bool pre = k < a.kv.prefix_len;
+  if (!pre) k -= a.kv.prefix_len;
+  const int pg = k / a.kv.page_rows;
+  const int id = __ldg((pre ? a.kv.prefix_pages : own_pages) + pg);
+  if (id < 0 || id >= a.kv.npages) return nullptr;
+  return static_cast<const uint16_t*>(a.kv.pool) +
+         (static_cast<int64_t>(id) * a.kv.page_rows + (k - pg * a.kv.page_rows)) * (2 * a.kv.kv_heads * D) + hk * D;
+}
+
+// Is a value of keys [k0, k1) not finite? By one whole warp.
+template <bool BF, int D>
+__device__ __noinline__ bool odd_values(const PagedAttnArgs& a, const int32_t* own_pages, int hk, int k0, int k1, int lane) {
+  float odd = 0.f;
+  for (int k = k0; k < k1; ++k) {
+    const uint16_t* row = key_row<D>(a, own_pages, hk, k);
+    if (row == nullptr) continue;
+    const uint32_t* v = reinterpret_cast<const uint32_t*>(row + a.kv.kv_heads * D) + lane * (D / 64);
+#pragma unroll
+    for (int i = 0; i < D / 64; ++i) {
+      const float2 x = unpack2<BF>(v[i]);
+      odd = fmaf(0.f, x.x, fmaf(0.f, x.y, odd));
+    }
+  }
+  return __any_sync(0xffffffffu, odd != odd);
+}
+
+// The sums of one query row over keys [k0, k1) alone, weights 2^(s - m): a
+// lane leaves values [lane D / 32, + D / 32). By one whole warp, key by key:
+// for the rare row that odd_values above sends here.
+template <bool BF, int D>
+__device__ __noinline__ void redo_row(const PagedAttnArgs& a, const int32_t* own_pages, int hk, int t, int h, int k0, int k1,
+                                      float m, int lane, float (&acc)[D / 32]) {
+  float2 q[D / 64];
+  const uint32_t* qr = reinterpret_cast<const uint32_t*>(static_cast<const uint16_t*>(a.q) +
+                                                         static_cast<int64_t>(t) * a.ldq + h * D) + lane * (D / 64);
+#pragma unroll
+  for (int i = 0; i < D / 64; ++i) {
+    q[i] = unpack2<BF>(qr[i]);
+    acc[2 * i] = acc[2 * i + 1] = 0.f;
+  }
+  const float base = m == -INFINITY ? 0.f : m;
+  for (int k = k0; k < k1; ++k) {
+    const uint16_t* row = key_row<D>(a, own_pages, hk, k);
+    const uint32_t* kr = reinterpret_cast<const uint32_t*>(row) + lane * (D / 64);
+    const uint32_t* vr = reinterpret_cast<const uint32_t*>(row + a.kv.kv_heads * D) + lane * (D / 64);
+    float s = 0.f;
+    if (row != nullptr)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const float2 x = unpack2<BF>(kr[i]);
+        s = fmaf(q[i].x, x.x, fmaf(q[i].y, x.y, s));
+      }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+    const float p = exp2f(fmaf(s, a.scale_log2, -base));
+    if (row != nullptr)
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        const float2 x = unpack2<BF>(vr[i]);
+        acc[2 * i] = fmaf(p, x.x, acc[2 * i]);
+        acc[2 * i + 1] = fmaf(p, x.y, acc[2 * i + 1]);
+      }
+  }
+}
 
 // Tiles of many rows on the tensor cores (k_paged_tc.cu).
 enum WideMode : int { WIDE_PREFIX = 0, WIDE_JOINT = 1 };

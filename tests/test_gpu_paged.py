@@ -301,6 +301,58 @@ def test_attention_runs(case):
     _attend(b, "f16", heads, vis=np.zeros(b.rows, np.int64))    # nothing at all
 
 
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("case", [([5], [20], 30, 8, 2, 128, 16), ([3, 6], [3, 90], 0, 4, 1, 64, 16),
+                                  ([150, 70], [170, 70], 100, 4, 2, 128, 16), ([140], [140], 0, 2, 1, 64, 64),
+                                  ([2] * 40, [9] * 40, 6000, 8, 2, 128, 64)],
+                         ids=["few", "few64", "many", "many64", "prefix"])
+def test_attention_odd_values_behind_the_mask(case, bad):
+    # K and V rows that are not finite, at keys that only a sequence's later
+    # rows see: the rows before them must not notice
+    counts, lens, prefix, heads, hk, d, page = case
+    b = P.Batch(counts, lens, prefix, hk, d, page, seed=21)
+    last = [m - 1 for m in lens]                      # seen by the last row alone
+    spots = [(s, m - (3 if n > 60 else 1)) for s, (n, m) in enumerate(zip(counts, lens))]
+    for s, i in spots:
+        b.pool[b.table[s, i // page], i % page, 1, :, 5] = bad
+    for s, m in enumerate(last):
+        b.pool[b.table[s, m // page], m % page, :, :, 7] = bad
+    pool = dev(b.pool, torch.bfloat16)
+    rng = np.random.default_rng(5)
+    qx = dev(rng.standard_normal((b.rows, heads, d)), torch.bfloat16)
+    out = torch.empty_like(qx)
+    kv = _paged(b, pool)
+    ws = torch.empty(q.attention_paged_bytes(kv, b.rows, heads), dtype=torch.uint8, device="cuda")
+    q.op_attention_paged(kv, qx, out, ws)
+    with np.errstate(invalid="ignore", over="ignore"):
+        want, bound = P.attention(b, host(pool), host(qx), b.seen(True), d ** -0.5, P.U["bf16"])
+    got = host(out)
+    ok = np.isfinite(want)
+    assert ok.any() and not ok.all()
+    assert np.all(np.abs(got[ok] - want[ok]) <= bound[ok])
+    assert not np.isfinite(got[~ok]).any()
+
+
+def test_attention_odd_values_behind_runs():
+    # leading runs of their own lengths over a prefix with such rows
+    b = P.Batch([40, 90], [40, 95], 300, 2, 128, 16, seed=22, stale=0.0)
+    for i in (77, 150):
+        b.pool[b.prefix_pages[i // 16], i % 16, 1, :, i % 128] = np.nan
+    pool = dev(b.pool, torch.float16)
+    kv = _paged(b, pool)
+    rng = np.random.default_rng(6)
+    qx = dev(rng.standard_normal((130, 8, 128)), torch.float16)
+    vis = rng.integers(0, 250, 130)
+    out = torch.empty_like(qx)
+    ws = torch.empty(q.attention_paged_bytes(kv, 130, 8), dtype=torch.uint8, device="cuda")
+    q.op_attention_paged(kv, qx, out, ws, vis=dev(vis.astype(np.int32)))
+    want, bound = P.attention(b, host(pool), host(qx), b.seen(False, vis), 128 ** -0.5, P.U["f16"])
+    got = host(out)
+    ok = np.isfinite(want)
+    assert np.all(np.abs(got[ok] - want[ok]) <= bound[ok])
+    assert not np.isfinite(got[~ok]).any()
+
+
 def test_attention_wide_scores_and_scale():
     # scores of +-100 and more: one key takes all the weight
     b = P.Batch([1, 50], [60, 70], 300, 2, 128, 16, amp=4.0, seed=11)
@@ -315,6 +367,25 @@ def test_attention_long_prefix_few_rows():
     _attend(b, "bf16", 8)
     b = P.Batch([1] * 30, [5] * 30, 9000, 1, 64, 64, seed=13)
     _attend(b, "f16", 8)
+
+
+@pytest.mark.parametrize("case", [
+    ([1] * 10, [40] * 10, 3000, 8, 2, 128, 64),         # prefix tiles of one CTA, 128-wide heads
+    ([2] * 12, [40] * 12, 5000, 8, 4, 64, 48),          # and 64-wide ones
+    ([1] * 90, [3] * 90, 2500, 4, 1, 128, 16),          # pairs of CTAs
+    ([9] * 60, [20] * 60, 1500, 16, 8, 128, 16),        # few-row tiles of 32 rows, behind a prefix
+    ([5] * 60, [33] * 60, 0, 32, 8, 64, 16),            # and without one
+    ([1, 0, 2], [5, 9, 40], 100, 160, 1, 64, 16),       # more heads to a key head than a tile has rows
+    ([100], [130], 40, 80, 1, 128, 32),                 # one token to a tile
+    ([1] * 33, [700] * 33, 0, 2, 1, 128, 16),           # parts of own keys
+], ids=["one", "one64", "pair", "two", "two64", "wide_group", "group80", "own_parts"])
+def test_attention_paths(case):
+    counts, lens, prefix, heads, hk, d, page = case
+    b = P.Batch(counts, lens, prefix, hk, d, page, seed=18)
+    _attend(b, "bf16", heads, pad=1)
+    rng = np.random.default_rng(19)
+    vis = rng.integers(0, prefix + max(lens) + 1, b.rows)
+    _attend(b, "f16", heads, vis=vis)
 
 
 def test_attention_reads_pages_past_32_bits():
