@@ -502,14 +502,22 @@ def op_attention(panel, heads, out, nq, n_own, kv_pre=None, n_pre=0, vis=None, s
 # each property of a tensor once (a call of a kernel of a few microseconds
 # must not wait for its Python side).
 
-def _paged_env(stream):
-    """(torch, current device, raw stream) of a call."""
-    import torch
-    dev = torch.cuda.current_device()
-    if stream is not None:
-        return torch, dev, stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
-    return torch, dev, raw(dev) if raw is not None else torch.cuda.current_stream().cuda_stream
+_env = None
+
+
+def _paged_env():
+    """(Tensor, current-device function, raw-stream function, int32, int64,
+    element types), looked up once."""
+    global _env
+    if _env is None:
+        import torch
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+        if raw is None:
+            def raw(dev):
+                return torch.cuda.current_stream(dev).cuda_stream
+        _env = (torch.Tensor, torch.cuda.current_device, raw, torch.int32, torch.int64,
+                {torch.bfloat16: B.ELEM_BF16, torch.float16: B.ELEM_F16, torch.float32: B.ELEM_F32})
+    return _env
 
 
 def _refuse_device(t, dev, name):
@@ -554,21 +562,13 @@ def _array(t, Tensor, dev, dtype, n, name):
     return t.data_ptr()
 
 
-def _elem(t):
-    torch = _torch()
-    e = {torch.bfloat16: B.ELEM_BF16, torch.float16: B.ELEM_F16, torch.float32: B.ELEM_F32}.get(t.dtype)
-    if e is None:
-        raise TypeError(f"expected an f32, f16 or bf16 tensor, got {t.dtype}")
-    return e
-
-
 def op_rope(r: Rope, x, pos, out=None, grad=False, stream=None):
     """qi21_op_rope: x [rows, heads, head_dim] (f32, f16 or bf16; rows may
     lie apart, as in a panel) turned by pos (int64 [rows], or [rows, 3] with
     three axes) into out (None: in place); grad=True turns a gradient back.
     Returns the output."""
-    torch, dev, st = _paged_env(stream)
-    T = torch.Tensor
+    T, cur, raw, _, i64, elems = _env or _paged_env()
+    dev = cur()
     dim = r.head_dim
     px, ldx, rows, heads = _rows_view(x, T, dev, dim, "x")
     if out is None or out is x:
@@ -577,10 +577,14 @@ def op_rope(r: Rope, x, pos, out=None, grad=False, stream=None):
         po, ldo, orows, oheads = _rows_view(out, T, dev, dim, "out")
         if orows != rows or oheads != heads or out.dtype != x.dtype:
             raise ValueError("out must have x's shape and dtype")
+    elem = elems.get(x.dtype)
+    if elem is None:
+        raise TypeError(f"x must be f32, f16 or bf16, got {x.dtype}")
     if heads == 0:
         return out
-    rc = load().qi21_op_rope(r, _elem(x), rows, heads, px, ldx, po, ldo,
-                             _array(pos, T, dev, torch.int64, rows * r.naxes, "pos"), 1 if grad else 0, st)
+    rc = (B._lib or load()).qi21_op_rope(r, elem, rows, heads, px, ldx, po, ldo,
+                                         _array(pos, T, dev, i64, rows * r.naxes, "pos"), 1 if grad else 0,
+                                         raw(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
     return out
@@ -594,8 +598,8 @@ class PagedKV:
     Keeps the tensors alive; their contents are read when the work runs."""
 
     def __init__(self, pool, table, lens, cu, prefix_pages=None, prefix_len=0):
-        torch, dev, _ = _paged_env(None)
-        T = torch.Tensor
+        T, cur, _, i32, _, _ = _paged_env()
+        dev = cur()
         c = B.Paged()
         c.pool = _array(pool, T, dev, getattr(pool, "dtype", None), pool.numel(), "pool")
         if pool.dim() != 5 or pool.shape[2] != 2:
@@ -606,9 +610,9 @@ class PagedKV:
         c.dtype = _dt_code(pool)
         c.npages, c.page_rows, _, c.kv_heads, c.head_dim = pool.shape
         c.nseq, c.table_stride = nseq, stride
-        c.table = _array(table, T, dev, torch.int32, nseq * stride, "table")
-        c.lens = _array(lens, T, dev, torch.int32, nseq, "lens")
-        c.cu = _array(cu, T, dev, torch.int32, nseq + 1, "cu")
+        c.table = _array(table, T, dev, i32, nseq * stride, "table")
+        c.lens = _array(lens, T, dev, i32, nseq, "lens")
+        c.cu = _array(cu, T, dev, i32, nseq + 1, "cu")
         c.prefix_len = prefix_len
         if prefix_len > 0:
             if prefix_pages is None:
@@ -616,26 +620,26 @@ class PagedKV:
             need = -(-prefix_len // c.page_rows) if c.page_rows else 0
             if prefix_pages.numel() < need:
                 raise ValueError(f"prefix_pages must have {need} entries, got {prefix_pages.numel()}")
-            c.prefix_pages = _array(prefix_pages, T, dev, torch.int32, prefix_pages.numel(), "prefix_pages")
+            c.prefix_pages = _array(prefix_pages, T, dev, i32, prefix_pages.numel(), "prefix_pages")
         self.c = c
         self.device = dev
         self.dtype = pool.dtype
         self._keep = (pool, table, lens, cu, prefix_pages)
 
 
-def _check_cache(kv, dev):
-    if kv.device != dev:
-        raise ValueError(f"the cache is on cuda:{kv.device}, the current device is cuda:{dev}")
+def _refuse_cache(kv, dev):
+    raise ValueError(f"the cache is on cuda:{kv.device}, the current device is cuda:{dev}")
 
 
 def op_kv_append(kv: PagedKV, k, v, rope=None, pos=None, stream=None):
     """qi21_op_kv_append: new keys (turned by rope at pos, int64; None: the
     rows' places in their sequences) and values, each [rows, kv_heads,
     head_dim], to their pages."""
-    torch, dev, st = _paged_env(stream)
-    T = torch.Tensor
+    T, cur, raw, _, i64, _ = _env or _paged_env()
+    dev = cur()
     c = kv.c
-    _check_cache(kv, dev)
+    if kv.device != dev:
+        _refuse_cache(kv, dev)
     dim = c.head_dim
     pk, ldk, rows, heads = _rows_view(k, T, dev, dim, "k")
     pv, ldv, vrows, vheads = _rows_view(v, T, dev, dim, "v")
@@ -645,8 +649,9 @@ def op_kv_append(kv: PagedKV, k, v, rope=None, pos=None, stream=None):
         raise TypeError("k and v must have the pool's dtype")
     pp = None
     if pos is not None:
-        pp = _array(pos, T, dev, torch.int64, rows * (1 if rope is None else rope.naxes), "pos")
-    rc = load().qi21_op_kv_append(c, rows, pk, ldk, pv, ldv, rope, pp, st)
+        pp = _array(pos, T, dev, i64, rows * (1 if rope is None else rope.naxes), "pos")
+    rc = (B._lib or load()).qi21_op_kv_append(c, rows, pk, ldk, pv, ldv, rope, pp,
+                                              raw(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
 
@@ -664,10 +669,11 @@ def op_attention_paged(kv: PagedKV, q, out, workspace, causal=True, vis=None, sc
     [prefix, own rows] of their sequences into out; scale defaults to
     1 / sqrt(head_dim). vis int32 [rows] (read as unsigned): leading runs in
     place of the causal ones."""
-    torch, dev, st = _paged_env(stream)
-    T = torch.Tensor
+    T, cur, raw, i32, _, _ = _env or _paged_env()
+    dev = cur()
     c = kv.c
-    _check_cache(kv, dev)
+    if kv.device != dev:
+        _refuse_cache(kv, dev)
     dim = c.head_dim
     pq, ldq, rows, heads = _rows_view(q, T, dev, dim, "q")
     po, ldo, orows, oheads = _rows_view(out, T, dev, dim, "out")
@@ -675,11 +681,15 @@ def op_attention_paged(kv: PagedKV, q, out, workspace, causal=True, vis=None, sc
         raise ValueError("out must have q's shape")
     if q.dtype != kv.dtype or out.dtype != kv.dtype:
         raise TypeError("q and out must have the pool's dtype")
-    nws = workspace.numel() * workspace.element_size()
-    pw = _array(workspace, T, dev, workspace.dtype, workspace.numel(), "workspace")
-    pvis = None if vis is None else _array(vis, T, dev, torch.int32, rows, "vis")
-    rc = load().qi21_op_attention_paged(c, rows, heads, pq, ldq, po, ldo, 1 if causal else 0, pvis,
-                                        dim ** -0.5 if scale is None else scale, pw, nws, st)
+    if not isinstance(workspace, T) or workspace.get_device() != dev:
+        _refuse_device(workspace, dev, "workspace")
+    if not workspace.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    pvis = None if vis is None else _array(vis, T, dev, i32, rows, "vis")
+    rc = (B._lib or load()).qi21_op_attention_paged(c, rows, heads, pq, ldq, po, ldo, 1 if causal else 0, pvis,
+                                                    dim ** -0.5 if scale is None else scale, workspace.data_ptr(),
+                                                    workspace.nbytes,
+                                                    raw(dev) if stream is None else stream.cuda_stream)
     if rc:
         check(rc)
 
