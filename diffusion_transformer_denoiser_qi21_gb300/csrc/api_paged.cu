@@ -81,15 +81,15 @@ static int check_paged(const qi21_paged* kv) {
   if (kv->kv_heads < 1 || kv->kv_heads > 1024) return refuse(QI21_ERR_GEOM, "kv_heads %d (1 .. 1024)", kv->kv_heads);
   if (kv->page_rows < 16 || kv->page_rows % 16 || kv->page_rows > (1 << 20))
     return refuse(QI21_ERR_GEOM, "page_rows %d (a multiple of 16)", kv->page_rows);
-  if (kv->npages < 0 || static_cast<int64_t>(kv->npages) * kv->page_rows > 0x7fffffff)
-    return refuse(QI21_ERR_SHAPE, "npages %d of %d rows (at most 2^31 - 1 rows in all)", kv->npages, kv->page_rows);
+  if (kv->npages < 1 || static_cast<int64_t>(kv->npages) * kv->page_rows > 0x7fffffff)
+    return refuse(QI21_ERR_SHAPE, "npages %d of %d rows (at least one page, at most 2^31 - 1 rows in all)", kv->npages, kv->page_rows);
   if (kv->nseq < 0 || kv->table_stride < 0 || kv->prefix_len < 0 || kv->prefix_len > (1 << 30))
     return refuse(QI21_ERR_SHAPE, "nseq %d table_stride %d prefix_len %d", kv->nseq, kv->table_stride, kv->prefix_len);
   return QI21_OK;
 }
 
 static int check_paged_ptrs(const qi21_paged* kv) {
-  if (!kv->cu || !kv->lens || (kv->table_stride > 0 && !kv->table) || (kv->npages > 0 && !kv->pool) ||
+  if (!kv->cu || !kv->lens || (kv->table_stride > 0 && !kv->table) || !kv->pool ||
       (kv->prefix_len > 0 && !kv->prefix_pages))
     return refuse(QI21_ERR_ARG, "null pointer in the paged cache");
   if (misaligned(kv->pool, 16)) return refuse(QI21_ERR_ARG, "the pool must be 16-byte aligned");

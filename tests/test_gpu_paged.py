@@ -1,5 +1,9 @@
 """The paged cache's kernels (rotation, append, shared-prefix attention)
 against plain 64-bit forms; the bounds are derived in tests/pagedcheck.py."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 
@@ -370,15 +374,16 @@ def test_attention_long_prefix_few_rows():
 
 
 @pytest.mark.parametrize("case", [
-    ([1] * 10, [40] * 10, 3000, 8, 2, 128, 64),         # prefix tiles of one CTA, 128-wide heads
-    ([2] * 12, [40] * 12, 5000, 8, 4, 64, 48),          # and 64-wide ones
+    ([1] * 10, [40] * 10, 3000, 8, 2, 128, 64),         # few-row tiles of the prefix
+    ([1] * 20, [40] * 20, 5000, 8, 2, 128, 64),         # prefix tiles of one CTA, 128-wide heads
+    ([2] * 24, [40] * 24, 9000, 8, 4, 64, 48),          # and 64-wide ones
     ([1] * 90, [3] * 90, 2500, 4, 1, 128, 16),          # pairs of CTAs
     ([9] * 60, [20] * 60, 1500, 16, 8, 128, 16),        # few-row tiles of 32 rows, behind a prefix
     ([5] * 60, [33] * 60, 0, 32, 8, 64, 16),            # and without one
     ([1, 0, 2], [5, 9, 40], 100, 160, 1, 64, 16),       # more heads to a key head than a tile has rows
     ([100], [130], 40, 80, 1, 128, 32),                 # one token to a tile
     ([1] * 33, [700] * 33, 0, 2, 1, 128, 16),           # parts of own keys
-], ids=["one", "one64", "pair", "two", "two64", "wide_group", "group80", "own_parts"])
+], ids=["few", "one", "one64", "pair", "two", "two64", "wide_group", "group80", "own_parts"])
 def test_attention_paths(case):
     counts, lens, prefix, heads, hk, d, page = case
     b = P.Batch(counts, lens, prefix, hk, d, page, seed=18)
@@ -451,6 +456,98 @@ def test_attention_repeats_bit_for_bit():
     b = P.Batch([1] * 20 + [150], [50] * 20 + [170], 3000, 2, 128, 16, seed=17)
     outs = [_attend(b, "bf16", 8)[1] for _ in range(2)]
     assert torch.equal(outs[0], outs[1])
+
+
+_FIRST = """
+import sys; sys.path.insert(0, {root!r})
+import torch
+import diffusion_transformer_denoiser_qi21_gb300 as q
+i = lambda x: torch.tensor(x, dtype=torch.int32, device="cuda")
+for n, prefix in ((1, 100), (1, 4000), (200, 100)):
+    pool = torch.randn(400, 16, 2, 2, 128, device="cuda").half()
+    kv = q.PagedKV(pool, i([[300 + k for k in range(20)]] * 30), i([n] * 30), i([n * k for k in range(31)]),
+                   prefix_pages=i(list(range(256))), prefix_len=prefix)
+    x, k = (torch.randn(30 * n, h, 128, device="cuda").half() for h in (8, 2))
+    out, pos = torch.empty_like(x), torch.arange(30 * n, device="cuda")
+    ws = torch.empty(q.attention_paged_bytes(kv, 30 * n, 8), dtype=torch.uint8, device="cuda")
+    r = q.rope(128)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):  # nothing of the library has run before
+        q.op_rope(r, x, pos)
+        q.op_kv_append(kv, k[:0], k[:0], rope=r)
+        q.op_attention_paged(kv, x, out, ws)
+    out.fill_(9)
+    y = x.clone()
+    g.replay()
+    torch.cuda.synchronize()
+    got = out.clone()
+    q.op_rope(r, y, pos)
+    q.op_attention_paged(kv, y, out, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(got, out) and q.device_status() == 0
+print("captured")
+"""
+
+
+def test_first_calls_inside_a_capture():
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", _FIRST.format(root=root)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
+
+
+def test_calls_of_two_streams_at_once():
+    # two batches over one pool, each with its workspace, on streams that run
+    # side by side
+    b = [P.Batch([1] * 30 + [40], [60] * 30 + [90], 4000, 2, 128, 16, seed=30 + i) for i in range(2)]
+    pools = [dev(x.pool, torch.bfloat16) for x in b]
+    kvs = [_paged(x, p) for x, p in zip(b, pools)]
+    xs = [dev(np.random.default_rng(40 + i).standard_normal((70, 8, 128)), torch.bfloat16) for i in range(2)]
+    ws = [torch.empty(q.attention_paged_bytes(k, 70, 8), dtype=torch.uint8, device="cuda") for k in kvs]
+    alone = []
+    for k, x, w in zip(kvs, xs, ws):
+        alone.append(torch.empty_like(x))
+        q.op_attention_paged(k, x, alone[-1], w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    outs = [torch.empty_like(x) for x in xs]
+    for _ in range(20):
+        for s, k, x, o, w in zip(streams, kvs, xs, outs, ws):
+            q.op_attention_paged(k, x, o, w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(alone, outs))
+
+
+def test_python_refusals():
+    b = P.Batch([2], [4], 10, 2, 64, 16, seed=1)
+    pool = dev(b.pool, torch.float16)
+    kv = _paged(b, pool)
+    x = torch.zeros(2, 4, 64, dtype=torch.float16, device="cuda")
+    ws = torch.empty(q.attention_paged_bytes(kv, 2, 4), dtype=torch.uint8, device="cuda")
+    k = torch.zeros(2, 2, 64, dtype=torch.float16, device="cuda")
+    r = q.rope(64)
+    pos = torch.zeros(2, dtype=torch.int64, device="cuda")
+    for bad in (lambda: q.op_attention_paged(kv, x.cpu(), x, ws), lambda: q.op_attention_paged(kv, x.float(), x, ws),
+                lambda: q.op_attention_paged(kv, x, x.bfloat16(), ws), lambda: q.op_kv_append(kv, k.float(), k),
+                lambda: q.op_rope(r, x.double(), pos), lambda: q.op_rope(r, x, pos.int()),
+                lambda: q.op_attention_paged(kv, x, x.clone(), ws, vis=pos)):
+        with pytest.raises(TypeError):
+            bad()
+    for bad in (lambda: q.op_attention_paged(kv, x, x[:1], ws), lambda: q.op_attention_paged(kv, x[..., :32], x, ws),
+                lambda: q.op_attention_paged(kv, x.transpose(0, 1), x, ws), lambda: q.op_kv_append(kv, x, x),
+                lambda: q.op_kv_append(kv, k, k[:1]), lambda: q.op_rope(r, x, pos[:1]),
+                lambda: q.op_rope(r, x[:1].expand(2, 4, 64), pos), lambda: q.op_rope(r, x, pos, out=x[:, :2]),
+                lambda: q.PagedKV(pool[0], dev(b.table), kv._keep[2], kv._keep[3]),
+                lambda: q.PagedKV(pool, dev(b.table), kv._keep[2][:0], kv._keep[3]),
+                lambda: q.PagedKV(pool, dev(b.table), kv._keep[2], kv._keep[3], prefix_len=5),
+                lambda: q.PagedKV(pool, dev(b.table), kv._keep[2], kv._keep[3], prefix_pages=kv._keep[4], prefix_len=99)):
+        with pytest.raises(ValueError):
+            bad()
+    with pytest.raises(q.Qi21Error) as e:
+        q.op_attention_paged(kv, x, x.clone(), ws[:256])
+    assert e.value.code == -8
+    with pytest.raises(q.Qi21Error):
+        q.attention_paged_bytes(kv, 2, 3)
 
 
 # --------------------------------------------------------------- together ----

@@ -103,7 +103,7 @@ def _paged(**kw):
 
 
 BAD = [(dict(dtype=2), -1), (dict(head_dim=96), -3), (dict(head_dim=256), -3), (dict(kv_heads=0), -3),
-       (dict(page_rows=0), -3), (dict(page_rows=24), -3), (dict(page_rows=8), -3), (dict(npages=-1), -2),
+       (dict(page_rows=0), -3), (dict(page_rows=24), -3), (dict(page_rows=8), -3), (dict(npages=-1), -2), (dict(npages=0), -2),
        (dict(npages=1 << 28), -2), (dict(nseq=-1), -2), (dict(table_stride=-1), -2), (dict(prefix_len=-1), -2),
        (dict(lens=None), -1), (dict(cu=None), -1), (dict(table=None), -1), (dict(pool=None), -1),
        (dict(prefix_pages=None), -1), (dict(pool=264), -1)]
