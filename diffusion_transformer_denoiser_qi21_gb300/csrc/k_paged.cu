@@ -752,7 +752,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   // a small call: one launch in which every sequence reads the prefix itself
   const int64_t again = own_tiles * hk * P * (4 * D);  // bytes of that
   const int64_t keys = static_cast<int64_t>(P) + a.kv.table_rows;
-  int64_t ncl = std::min<int64_t>(2 * static_cast<int64_t>(sm_count()) / (own_tiles * hk), keys / 128);
+  int64_t ncl = std::min<int64_t>(3 * static_cast<int64_t>(sm_count()) / (own_tiles * hk), keys / 64);
   ncl = ncl >= 8 ? 8 : ncl >= 4 ? 4 : ncl >= 2 ? 2 : 1;
   if (again <= kReadAgain && keys <= 1024 * ncl && own_tiles * hk * ncl <= 0x7fffffff) {
     a.cluster = static_cast<int>(ncl);
