@@ -232,7 +232,10 @@ __global__ void __launch_bounds__(kWarps * 32) attn_paged_narrow(const __grid_co
     g0 = static_cast<int>(static_cast<int64_t>(ng) * split / ncl);
     g1 = static_cast<int>(static_cast<int64_t>(ng) * (split + 1) / ncl);
   } else {
-    const int part = (pre ? a.pre_keys : a.own_keys) / kGran;
+    // equal parts of the longest sequence that the table can hold; a shorter
+    // one is cut as often, but into parts of 256 keys at least
+    int part = (pre ? a.pre_keys : a.own_keys) / kGran;
+    if (!pre) part = min(part, max(256 / kGran, (ng + a.own_splits - 1) / a.own_splits));
     const int64_t k0 = static_cast<int64_t>(split) * part;
     g0 = static_cast<int>(min(k0, static_cast<int64_t>(ng)));
     g1 = static_cast<int>(min(k0 + part, static_cast<int64_t>(ng)));
@@ -750,7 +753,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   const int64_t own_tiles = pairs / R + seqs;
   a.own_tiles = static_cast<int>(own_tiles);
   // a small call: one launch in which every sequence reads the prefix itself
-  const int64_t again = own_tiles * hk * P * (4 * D);  // bytes of that
+  const double again = static_cast<double>(own_tiles) * hk * P * (4 * D);  // bytes of that
   const int64_t keys = static_cast<int64_t>(P) + a.kv.table_rows;
   int64_t ncl = std::min<int64_t>(3 * static_cast<int64_t>(sm_count()) / (own_tiles * hk), keys / 64);
   ncl = ncl >= 8 ? 8 : ncl >= 4 ? 4 : ncl >= 2 ? 2 : 1;
@@ -771,7 +774,8 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     *part = static_cast<int>(((keys + n - 1) / n + kGran - 1) / kGran * kGran);
     return static_cast<int>(n);
   };
-  const int64_t few = (pairs + R - 1) / R * P * hk * (4 * D);  // bytes that few-row tiles of the prefix read
+  // bytes that few-row tiles of the prefix read
+  const double few = static_cast<double>((pairs + R - 1) / R) * P * hk * (4 * D);
   const bool wide = P > 0 && tokens > 0 && pairs > R && few > kFewRowPrefix;
   const bool pair = D == 128 && pairs > 128;
   const int per = tokens * (pair ? 2 : 1);
@@ -788,10 +792,10 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   a.own_splits = splits(a.own_tiles, a.kv.table_rows, most - a.pre_splits, &a.own_keys);
   a.slots = a.pre_splits + a.own_splits;
   place_parts();
-  if (wide && (e = launch_attn_wide(a, WIDE_PREFIX, pair, wide_tiles, a.pre_splits, s)) != cudaSuccess) return e;
   const int64_t gx = hk * (static_cast<int64_t>(a.pre_tiles) * a.pre_splits +
                            static_cast<int64_t>(a.own_tiles) * a.own_splits);
   if (gx > 0x7fffffff) return cudaErrorInvalidValue;
+  if (wide && (e = launch_attn_wide(a, WIDE_PREFIX, pair, wide_tiles, a.pre_splits, s)) != cudaSuccess) return e;
   a.first = !wide;
   e = narrow(gx, 1);
   return e != cudaSuccess || a.slots == 1 ? e : join();

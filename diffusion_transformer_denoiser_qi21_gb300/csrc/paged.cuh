@@ -68,25 +68,28 @@ struct PagedAttnArgs {
 // The x-th tile, counted over the sequences in order, of `tile` of the `per`
 // pieces that a row has: its sequence b and its place `at` there, the
 // sequence's first row and rows in this call, and its length as given; by
-// one whole warp (32 sequences per round, all of their numbers loaded at
-// once). b == nseq: there are fewer tiles.
+// one whole warp (128 sequences per round, all of their numbers loaded at
+// once: a round is a wait for memory). b == nseq: there are fewer tiles.
 struct SeqTile {
   int b, at, row0, rows, len;
 };
 __device__ __forceinline__ SeqTile warp_find_tile(const PagedAttnArgs& a, int x, int per, int tile, int lane) {
-  SeqTile r{a.kv.nseq, 0, 0, 0, 0};
   int before = 0;
-  for (int b0 = 0; b0 < a.kv.nseq; b0 += 32) {
-    int c0 = 0, rows = 0, len = 0;
-    if (b0 + lane < a.kv.nseq) {
-      c0 = __ldg(a.kv.cu + b0 + lane);
-      len = __ldg(a.kv.lens + b0 + lane);
-      const int c1 = __ldg(a.kv.cu + b0 + lane + 1);
+  for (int b0 = 0; b0 < a.kv.nseq; b0 += 128) {
+    const int b = b0 + 4 * lane;  // this lane's four sequences
+    int c[5], len[4], n[4];
+#pragma unroll
+    for (int k = 0; k < 5; ++k) c[k] = b + k <= a.kv.nseq ? __ldg(a.kv.cu + b + k) : 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) len[k] = b + k < a.kv.nseq ? __ldg(a.kv.lens + b + k) : 0;
+    int mine = 0;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
       // ends that do not fit the call's rows: no rows
-      rows = (c0 >= 0 && c1 <= a.rows && c1 > c0) ? c1 - c0 : 0;
+      n[k] = b + k < a.kv.nseq && c[k] >= 0 && c[k + 1] <= a.rows && c[k + 1] > c[k] ? c[k + 1] - c[k] : 0;
+      mine += (n[k] * per + tile - 1) / tile;
     }
-    const int n = (rows * per + tile - 1) / tile;
-    int sum = n;
+    int sum = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(0xffffffffu, sum, o);
@@ -95,16 +98,22 @@ __device__ __forceinline__ SeqTile warp_find_tile(const PagedAttnArgs& a, int x,
     const unsigned past = __ballot_sync(0xffffffffu, before + sum > x);
     if (past) {
       const int l = __ffs(past) - 1;
-      r.b = b0 + l;
-      r.at = x - before - __shfl_sync(0xffffffffu, sum - n, l);
-      r.row0 = __shfl_sync(0xffffffffu, c0, l);
-      r.rows = __shfl_sync(0xffffffffu, rows, l);
-      r.len = __shfl_sync(0xffffffffu, len, l);
+      SeqTile r{b, x - before - (sum - mine), c[0], n[0], len[0]};  // lane l's is right
+#pragma unroll
+      for (int k = 0; k < 3; ++k) {
+        const int t = (n[k] * per + tile - 1) / tile;
+        if (r.b == b + k && r.at >= t) r = SeqTile{b + k + 1, r.at - t, c[k + 1], n[k + 1], len[k + 1]};
+      }
+      r.b = __shfl_sync(0xffffffffu, r.b, l);
+      r.at = __shfl_sync(0xffffffffu, r.at, l);
+      r.row0 = __shfl_sync(0xffffffffu, r.row0, l);
+      r.rows = __shfl_sync(0xffffffffu, r.rows, l);
+      r.len = __shfl_sync(0xffffffffu, r.len, l);
       return r;
     }
     before += __shfl_sync(0xffffffffu, sum, 31);
   }
-  return r;
+  return SeqTile{a.kv.nseq, 0, 0, 0, 0};
 }
 
 // Programmatic launch: a call's kernels may start while the one before them

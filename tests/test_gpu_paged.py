@@ -383,7 +383,9 @@ def test_attention_long_prefix_few_rows():
     ([1, 0, 2], [5, 9, 40], 100, 160, 1, 64, 16),       # more heads to a key head than a tile has rows
     ([100], [130], 40, 80, 1, 128, 32),                 # one token to a tile
     ([1] * 33, [700] * 33, 0, 2, 1, 128, 16),           # parts of own keys
-], ids=["few", "one", "one64", "pair", "two", "two64", "wide_group", "group80", "own_parts"])
+    ([0, 1, 2] * 100, [3, 1, 40] * 100, 20, 2, 1, 64, 16),   # more sequences than one round finds
+    ([0, 30, 0, 0, 90] * 60, [1, 30, 0, 9, 95] * 60, 0, 1, 1, 64, 16),
+], ids=["few", "one", "one64", "pair", "two", "two64", "wide_group", "group80", "own_parts", "rounds", "rounds_many"])
 def test_attention_paths(case):
     counts, lens, prefix, heads, hk, d, page = case
     b = P.Batch(counts, lens, prefix, hk, d, page, seed=18)
@@ -391,6 +393,19 @@ def test_attention_paths(case):
     rng = np.random.default_rng(19)
     vis = rng.integers(0, prefix + max(lens) + 1, b.rows)
     _attend(b, "f16", heads, vis=vis)
+
+
+def test_attention_in_a_table_far_larger_than_its_sequences():
+    b = P.Batch([1, 3, 1], [700, 40, 3], 500, 2, 64, 16, seed=23)
+    wide = np.full((3, 3000), -1, np.int32)
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    _attend(b, "bf16", 4)
+    b = P.Batch([100], [120], 500, 2, 128, 16, seed=24)
+    wide = np.full((1, 3000), -1, np.int32)
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    _attend(b, "f16", 4)
 
 
 def test_attention_reads_pages_past_32_bits():
