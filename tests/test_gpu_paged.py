@@ -511,6 +511,39 @@ def test_first_calls_inside_a_capture():
     assert r.returncode == 0 and "captured" in r.stdout, r.stderr[-2000:]
 
 
+@pytest.mark.parametrize("case", [([1] * 4, [9] * 4, 100), ([1] * 40, [50] * 40, 6000), ([90, 20], [90, 70], 100)],
+                         ids=["small", "parts", "many"])
+def test_captures_that_fork_and_that_start_with_a_call(case):
+    # the call alone in a graph; in two branches of one; behind a copy
+    counts, lens, prefix = case
+    b = P.Batch(counts, lens, prefix, 2, 128, 16, seed=33)
+    pool = dev(b.pool, torch.bfloat16)
+    kv = _paged(b, pool)
+    x = dev(np.random.default_rng(34).standard_normal((b.rows, 8, 128)), torch.bfloat16)
+    new = lambda: (torch.zeros_like(x),  # noqa: E731
+                   torch.empty(q.attention_paged_bytes(kv, b.rows, 8), dtype=torch.uint8, device="cuda"))
+    (want, w0), (o1, w1), (o2, w2), (o3, w3) = new(), new(), new(), new()
+    q.op_attention_paged(kv, x, want, w0)
+    torch.cuda.synchronize()
+    alone, forked = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(alone):
+        q.op_attention_paged(kv, x, o1, w1)
+    y = torch.zeros_like(x)
+    with torch.cuda.graph(forked):
+        main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+        side.wait_stream(main)
+        q.op_attention_paged(kv, x, o2, w2, stream=side)
+        y.copy_(x)
+        q.op_attention_paged(kv, y, o3, w3)
+        main.wait_stream(side)
+        o3.add_(o2)
+    for _ in range(3):
+        alone.replay()
+        forked.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o1, want) and torch.equal(o2, want) and torch.equal(o3, want + want)
+
+
 def test_calls_of_two_streams_at_once():
     # two batches over one pool, each with its workspace, on streams that run
     # side by side
