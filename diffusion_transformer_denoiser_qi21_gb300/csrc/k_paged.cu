@@ -650,10 +650,11 @@ size_t attn_paged_bytes(const PagedArgs& p, int rows, int heads) {
 // of its key blocks; the few-row tiles that run beside it take `beside`
 // SM-microseconds (their lengths are known to the device alone: half the
 // table's rows is assumed, so a count that makes the wide part itself 1.6
-// times longer than need be is out); parts are written and read back at
+// times longer than need be is out); a join takes 4 us (a call that is joined
+// anyway has it whatever the count), and parts are written and read back at
 // about 4 TB/s. Fewer parts pay `fixed` less often, more fill the GPU.
-static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block, double beside, int64_t rows_heads,
-                       int dim, int most) {
+static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block, bool joined, double beside,
+                       int64_t rows_heads, int dim, int most) {
   const double fixed = 8.0, sms = sm_count();
   double least = 0.0;
   int best = 1;
@@ -667,7 +668,7 @@ static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block
         if (n == 1 || alone < least) least = alone;
       } else if (alone <= 1.6 * least) {
         const double t = std::max(alone, (all * one + beside) / sms) +
-                         (n > 1 || beside > 0 ? n * static_cast<double>(rows_heads) * dim * 8 / 4e6 : 0.0);
+                         (n > 1 || joined ? 4.0 + n * static_cast<double>(rows_heads) * dim * 8 / 4e6 : 0.0);
         if (got == 0.0 || t < got) {
           got = t;
           best = n;
@@ -720,7 +721,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   const int most = paged_slots(a.rows);
   const int tokens = wide_tokens(a.group);
   cudaError_t e = cudaSuccess;
-  auto block_us = [](bool pair) { return D == 64 ? 0.65 : pair ? 0.8 : 1.3; };  // measured
+  auto block_us = [](bool pair) { return D == 64 ? 0.7 : pair ? 0.8 : 0.75; };  // measured
   auto join = [&] {
     const int warps = a.slots > 32 ? 8 : a.slots > 16 ? 4 : a.slots > 8 ? 2 : 1;
     return launch_early(attn_paged_join<BF, D>, static_cast<unsigned>((all * warps + 7) / 8), 256, 0, s, 1, a, warps);
@@ -729,15 +730,29 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     a.part_ml = reinterpret_cast<float2*>(a.part_o + static_cast<int64_t>(a.slots) * a.rows * a.heads * D);
   };
   if (tokens > 0 && pairs >= 64 * static_cast<int64_t>(seqs)) {
-    // many rows per sequence: a sequence's tiles walk [prefix, own keys]
-    const bool pair = D == 128 && pairs > 128 * static_cast<int64_t>(seqs);
+    // many rows per sequence: a sequence's tiles walk [prefix, own keys]. The
+    // CTAs stay for several items, as pairs, if there are items enough (the
+    // sequences taken as equal) and the keys fit the L2 (129 MB): then in
+    // order of tiles, a sequence's last ones, which see the most keys, of all
+    // heads first. Three prompts of 1250 rows behind 2048, 8 key heads: 158 us
+    // against 172 with an item a CTA, and 167 with single CTAs; of 700 behind
+    // 905, 32 key heads (54 MB): 66 against 79. Else the tiles of one head run
+    // together, which read the same keys, and single CTAs need no partner in
+    // step: four images of 1024 rows behind 4114, 32 heads (134 MB): 255
+    // against 265 as pairs, and 284 if they stay
+    const int64_t blocks = (static_cast<int64_t>(P) + 127) / 128 + (static_cast<int64_t>(a.kv.table_rows) + 127) / 128;
+    const double kv_bytes = (P + static_cast<double>(a.kv.nseq) * a.kv.table_rows) * hk * (4 * D);
+    const int64_t each = (a.rows + static_cast<int64_t>(seqs) - 1) / seqs;  // rows of a sequence
+    auto items = [&](bool pair) { return seqs * ((each + tokens * (pair ? 2 : 1) - 1) / (tokens * (pair ? 2 : 1))) * hk; };
+    const bool two_tiles = D == 128 && pairs > 128 * static_cast<int64_t>(seqs);
+    const bool stay = kv_bytes <= (96 << 20) && items(two_tiles) > sm_count() / (two_tiles ? 2 : 1);
+    const bool pair = two_tiles && stay;
     const int per = tokens * (pair ? 2 : 1);
     const int64_t tiles = a.rows / per + seqs;
-    const int64_t blocks = (static_cast<int64_t>(P) + 127) / 128 + (static_cast<int64_t>(a.kv.table_rows) + 127) / 128;
     if (tiles > 0x3fffffff / kMaxSlots) return cudaErrorInvalidValue;
-    a.slots = wide_splits(tiles * hk, pair ? 2 : 1, blocks, block_us(pair), 0.0, all, D, most);
+    a.slots = stay ? 1 : wide_splits(items(pair), pair ? 2 : 1, blocks, block_us(pair), false, 0.0, all, D, most);
     place_parts();
-    e = launch_attn_wide(a, WIDE_JOINT, pair, static_cast<int>(tiles), a.slots, s);
+    e = launch_attn_wide(a, stay ? WIDE_STAY : WIDE_JOINT, pair, static_cast<int>(tiles), a.slots, s);
     return e != cudaSuccess || a.slots == 1 ? e : join();
   }
   // tiles of 16 rows, or of 32 where a sequence has more and there are tiles
@@ -784,7 +799,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     wide_tiles = (a.rows + per - 1) / per;
     const double own_bytes = 0.5 * seqs * a.kv.table_rows * hk * (4.0 * D);
     a.pre_splits = wide_splits(static_cast<int64_t>(wide_tiles) * hk, pair ? 2 : 1, (static_cast<int64_t>(P) + 127) / 128,
-                               block_us(pair), own_bytes / 30e3, all, D, most - 1);
+                               block_us(pair), true, own_bytes / 30e3, all, D, most - 1);
   } else if (P > 0) {
     a.pre_tiles = static_cast<int>((pairs + R - 1) / R);
     a.pre_splits = splits(a.pre_tiles, P, most - 1, &a.pre_keys);

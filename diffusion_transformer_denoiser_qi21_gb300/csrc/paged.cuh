@@ -192,7 +192,7 @@ __device__ __noinline__ void redo_row(const PagedAttnArgs& a, const int32_t* own
 }
 
 // Tiles of many rows on the tensor cores (k_paged_tc.cu).
-enum WideMode : int { WIDE_PREFIX = 0, WIDE_JOINT = 1 };
+enum WideMode : int { WIDE_PREFIX = 0, WIDE_JOINT = 1, WIDE_STAY = 2 };  // STAY: joint, for several items
 // Tokens of a CTA's tile, 0 if the group does not fit one.
 inline int wide_tokens(int group) { return group <= 128 ? 128 / group : 0; }
 cudaError_t launch_attn_wide(const PagedAttnArgs& a, WideMode mode, bool pair, int tiles, int splits, cudaStream_t s);
