@@ -536,6 +536,8 @@ def _rows_view(t, Tensor, dev, dim, name):
     if len(shape) != 3 or shape[2] != dim:
         raise ValueError(f"{name} must be [rows, heads, {dim}], got {tuple(shape)}")
     rows, heads, _ = shape
+    if rows > 0x7fffffff:
+        raise ValueError(f"{name} has more than 2^31 - 1 rows")
     wide = heads * dim
     ld, sh, se = t.stride()
     if rows and wide and (se != 1 or (heads > 1 and sh != dim)):
@@ -580,6 +582,8 @@ def op_rope(r: Rope, x, pos, out=None, grad=False, stream=None):
     elem = elems.get(x.dtype)
     if elem is None:
         raise TypeError(f"x must be f32, f16 or bf16, got {x.dtype}")
+    if r.naxes == 3 and getattr(pos, "shape", (3,))[-1:] != (3,):
+        raise ValueError(f"pos must be [rows, 3], got {tuple(pos.shape)}")
     if heads == 0:
         return out
     rc = (B._lib or load()).qi21_op_rope(r, elem, rows, heads, px, ldx, po, ldo,
@@ -607,6 +611,8 @@ class PagedKV:
         if table.dim() != 2:
             raise ValueError("table must be [nseq, pages]")
         nseq, stride = table.shape
+        if not 0 <= prefix_len < 1 << 30:
+            raise ValueError(f"prefix_len {prefix_len} (0 .. 2^30 - 1)")
         c.dtype = _dt_code(pool)
         c.npages, c.page_rows, _, c.kv_heads, c.head_dim = pool.shape
         c.nseq, c.table_stride = nseq, stride
@@ -649,6 +655,8 @@ def op_kv_append(kv: PagedKV, k, v, rope=None, pos=None, stream=None):
         raise TypeError("k and v must have the pool's dtype")
     pp = None
     if pos is not None:
+        if rope is not None and rope.naxes == 3 and getattr(pos, "shape", (3,))[-1:] != (3,):
+            raise ValueError(f"pos must be [rows, 3], got {tuple(pos.shape)}")
         pp = _array(pos, T, dev, i64, rows * (1 if rope is None else rope.naxes), "pos")
     rc = (B._lib or load()).qi21_op_kv_append(c, rows, pk, ldk, pv, ldv, rope, pp,
                                               raw(dev) if stream is None else stream.cuda_stream)

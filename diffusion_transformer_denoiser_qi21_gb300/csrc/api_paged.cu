@@ -83,7 +83,7 @@ static int check_paged(const qi21_paged* kv) {
     return refuse(QI21_ERR_GEOM, "page_rows %d (a multiple of 16)", kv->page_rows);
   if (kv->npages < 1 || static_cast<int64_t>(kv->npages) * kv->page_rows > 0x7fffffff)
     return refuse(QI21_ERR_SHAPE, "npages %d of %d rows (at least one page, at most 2^31 - 1 rows in all)", kv->npages, kv->page_rows);
-  if (kv->nseq < 0 || kv->table_stride < 0 || kv->prefix_len < 0 || kv->prefix_len > (1 << 30))
+  if (kv->nseq < 0 || kv->table_stride < 0 || kv->prefix_len < 0 || kv->prefix_len >= (1 << 30))
     return refuse(QI21_ERR_SHAPE, "nseq %d table_stride %d prefix_len %d", kv->nseq, kv->table_stride, kv->prefix_len);
   return QI21_OK;
 }
@@ -243,7 +243,7 @@ int qi21_op_attention_paged(const qi21_paged* kv, int32_t rows, int32_t heads, c
   if (ldq < wide || ldo < wide || ldq % 8 || ldo % 8)
     return refuse(QI21_ERR_SHAPE, "ldq %lld ldo %lld (at least heads * head_dim %lld, multiples of 8)",
                   static_cast<long long>(ldq), static_cast<long long>(ldo), static_cast<long long>(wide));
-  if (!(scale > 0.f) || !std::isfinite(scale)) return refuse(QI21_ERR_ARG, "scale must be > 0 and finite");
+  if (!(scale > 0.f) || !(scale <= 1e38f)) return refuse(QI21_ERR_ARG, "scale must be > 0 and at most 1e38");
   if (rows == 0 || kv->nseq == 0) return QI21_OK;
   if (!q || !out) return refuse(QI21_ERR_ARG, "null pointer");
   if (misaligned(q, 16) || misaligned(out, 16)) return refuse(QI21_ERR_ARG, "q and out must be 16-byte aligned");

@@ -633,8 +633,8 @@ typedef struct qi21_rope {
 /* Fills *r on the host. axes: NULL for one position per row, else the three
  * axis widths (even, summing to rot_dim; pairs in axis order, as
  * qi21_geom::axes). kind: a frequency rule; factor >= 1 (finite); orig_len,
- * fast_turns > slow_turns > 0 are read by RAMP and BAND only (an fast_turns
- * and slow_turns of 0 stand for 32 and 1 in RAMP, 4 and 1 in BAND).
+ * fast_turns > slow_turns > 0 are read by RAMP and BAND only (fast_turns and
+ * slow_turns of 0 stand for 32 and 1 in RAMP, 4 and 1 in BAND).
  * out_scale: 0 stands for 0.1 ln(factor) + 1 in RAMP and 1 otherwise.
  * base > 1. */
 int qi21_rope_init(qi21_rope* r, int32_t head_dim, int32_t rot_dim, int32_t layout, const int32_t* axes,
@@ -680,7 +680,7 @@ typedef struct qi21_paged {
   const int32_t* lens;         /* device [nseq] own rows, the call's among them */
   const int32_t* cu;           /* device [nseq + 1] first row of each sequence, non-decreasing from 0 */
   const int32_t* prefix_pages; /* device [ceil(prefix_len / page_rows)], NULL if prefix_len == 0 */
-  int32_t prefix_len;
+  int32_t prefix_len;          /* below 2^30; so are the own rows that are read */
 } qi21_paged;
 
 /* Writes the call's `rows` new keys and values (k, v: dtype [rows][kv_heads]
@@ -701,11 +701,11 @@ size_t qi21_attention_paged_bytes(const qi21_paged* kv, int32_t rows, int32_t he
  * sharing key head h (g = heads / kv_heads). Query row t sees a leading run
  * of its keys: all of them, with causal != 0 those up to its own row, with
  * vis (device uint32 [rows], takes the place of causal) the first
- * min(vis[t], keys). A row that sees no key is 0. q dtype [rows][heads]
- * [head_dim] with ldq elements from row to row, out likewise with ldo (must
- * not overlap q); both 16-byte aligned, ldq and ldo multiples of 8. scale
- * > 0 and finite. f32 scores, softmax and sums. When the rows of a sequence
- * are few the prefix's part is computed once for the rows of all sequences;
+ * min(vis[t], keys). A row that sees no key is 0, and so is one whose
+ * scores are all minus infinity. q dtype [rows][heads][head_dim] with ldq
+ * elements from row to row, out likewise with ldo (must not overlap q); both
+ * 16-byte aligned, ldq and ldo multiples of 8. scale > 0, at most 1e38. f32
+ * scores, softmax and sums. When the rows of a sequence are few the prefix's part is computed once for the rows of all sequences;
  * parts meet in the workspace (device, 256-byte aligned, at least
  * qi21_attention_paged_bytes; needs no initial value; calls, or graphs, that
  * share one must not overlap in time). Values behind a sequence's end, in

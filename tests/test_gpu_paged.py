@@ -566,6 +566,101 @@ def test_calls_of_two_streams_at_once():
     assert all(torch.equal(x, y) for x, y in zip(alone, outs))
 
 
+# Tiles of many rows with more items than there are CTAs (a CTA then takes
+# several of them): as pairs of CTAs, as single ones for 64-wide heads and for
+# one tile a sequence; ragged, with an empty sequence and one of a single row.
+STAYS = [
+    ([300, 0, 140, 1, 77], [300, 9, 333, 1, 90], 300, 64, 16, 128, 16),
+    ([200, 317], [211, 317], 70, 64, 32, 64, 48),
+    ([30] * 39 + [31], list(range(40, 80)), 130, 16, 4, 128, 64),
+]
+STAY_IDS = ["pair", "single64", "single128"]
+
+
+@pytest.mark.parametrize("case", STAYS, ids=STAY_IDS)
+def test_attention_several_items_a_cta(case):
+    counts, lens, prefix, heads, hk, d, page = case
+    b = P.Batch(counts, lens, prefix, hk, d, page, seed=41)
+    _attend(b, "bf16", heads, pad=3)
+    rng = np.random.default_rng(42)
+    vis = rng.integers(0, prefix + max(lens) + 1, b.rows)
+    vis[: b.rows // 3] = 0  # items without keys among the others
+    _attend(b, "f16", heads, vis=vis, pad=1)
+    # the same batch in a table of many more rows: an item to a CTA
+    wide = np.full((len(counts), 40000 // page), -1, np.int32)
+    wide[:, :b.table.shape[1]] = b.table
+    b.table = wide
+    _attend(b, "bf16", heads)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), -float("inf")])
+@pytest.mark.parametrize("case", [([150, 90] * 10, [170, 90] * 10, 100, 16, 4, 128, 16),
+                                  ([130] * 13, [150] * 13, 0, 12, 12, 64, 64)], ids=["pair", "single64"])
+def test_attention_several_items_a_cta_odd_values(case, bad):
+    test_attention_odd_values_behind_the_mask(case, bad)
+
+
+@pytest.mark.parametrize("copies", [1, 20], ids=["item", "items"])
+def test_attention_many_rows_bad_pages_read_as_zeros(copies):
+    # whole pages and the one that the end cuts (rows 144 .. 149)
+    b = P.Batch([140] * copies, [150] * copies, 64, 4, 128, 16, seed=43, stale=0.0)
+    pool = dev(b.pool, torch.float16)
+    b.table[0, 1], b.table[0, 9], b.table[copies - 1, 3], b.prefix_pages[2] = pool.shape[0] + 5, -1, -7, pool.shape[0]
+    bad = [(0, 1), (0, 9), (copies - 1, 3)]
+    kv = _paged(b, pool)
+    qx = dev(np.random.default_rng(1).standard_normal((b.rows, 8, 128)), torch.float16)
+    out = torch.empty_like(qx)
+    ws = torch.empty(q.attention_paged_bytes(kv, b.rows, 8), dtype=torch.uint8, device="cuda")
+    q.op_attention_paged(kv, qx, out, ws)
+    assert q.device_status() == 2
+    zero = torch.cat([pool, torch.zeros_like(pool[:1])])
+    for at in bad:
+        b.table[at] = pool.shape[0]
+    b.prefix_pages[2] = pool.shape[0]
+    want, bound = P.attention(b, host(zero), host(qx), b.seen(True), 128 ** -0.5, P.U["f16"])
+    assert np.all(np.abs(host(out) - want) <= bound)
+
+
+def test_attention_many_rows_past_32_bits():
+    # a pool of more than 2^31 values, the used pages at its end
+    page, hk, d = 256, 8, 128
+    n = (1 << 31) // (page * 2 * hk * d) + 6
+    pool = torch.zeros(n, page, 2, hk, d, dtype=torch.bfloat16, device="cuda")
+    b = P.Batch([200, 30], [299, 30], 100, hk, d, page, seed=44)
+    last = n - b.pool.shape[0]
+    pool[last:] = dev(b.pool, torch.bfloat16)
+    tail = pool[last:]
+    small = b.table.copy(), b.prefix_pages.copy()
+    b.table = np.where(b.table >= 0, b.table + last, -1).astype(np.int32)
+    b.prefix_pages = (b.prefix_pages + last).astype(np.int32)
+    kv = _paged(b, pool)
+    b.table, b.prefix_pages = small
+    _attend(b, "bf16", 16, kv=kv, pool=tail)
+
+
+def test_captures_of_several_items_a_cta():
+    test_captures_that_fork_and_that_start_with_a_call(([90] * 20, [95] * 20, 100))
+
+
+def test_several_items_a_cta_on_two_streams():
+    b = P.Batch([90] * 20, [95] * 20, 500, 4, 128, 16, seed=45)
+    pool = dev(b.pool, torch.bfloat16)
+    kv = _paged(b, pool)
+    xs = [dev(np.random.default_rng(46 + i).standard_normal((b.rows, 8, 128)), torch.bfloat16) for i in range(2)]
+    ws = [torch.empty(q.attention_paged_bytes(kv, b.rows, 8), dtype=torch.uint8, device="cuda") for _ in xs]
+    alone = [torch.empty_like(x) for x in xs]
+    for x, w, o in zip(xs, ws, alone):
+        q.op_attention_paged(kv, x, o, w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in xs]
+    outs = [torch.empty_like(x) for x in xs]
+    for _ in range(20):
+        for s, x, o, w in zip(streams, xs, outs, ws):
+            q.op_attention_paged(kv, x, o, w, stream=s)
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, y) for x, y in zip(alone, outs))
+
+
 def test_python_refusals():
     b = P.Batch([2], [4], 10, 2, 64, 16, seed=1)
     pool = dev(b.pool, torch.float16)
@@ -596,6 +691,25 @@ def test_python_refusals():
     assert e.value.code == -8
     with pytest.raises(q.Qi21Error):
         q.attention_paged_bytes(kv, 2, 3)
+
+
+def test_python_refusals_of_lengths_and_positions():
+    b = P.Batch([2], [4], 10, 2, 64, 16, seed=1)
+    pool = dev(b.pool, torch.float16)
+    for n in (-1, 1 << 30, (1 << 32) + 5):
+        with pytest.raises(ValueError):
+            q.PagedKV(pool, dev(b.table), dev(np.array([4], np.int32)), dev(b.cu),
+                      prefix_pages=dev(b.prefix_pages), prefix_len=n)
+    r = q.rope(64, axes=(16, 24, 24))
+    x = torch.zeros(2, 2, 64, dtype=torch.float16, device="cuda")
+    pos = torch.zeros(3, 2, dtype=torch.int64, device="cuda")
+    with pytest.raises(ValueError):
+        q.op_rope(r, x, pos)
+    with pytest.raises(ValueError):
+        q.op_kv_append(_paged(b, pool), x, x, rope=r, pos=pos)
+    many = torch.zeros(1, 1, 64, dtype=torch.float16, device="cuda").expand((1 << 32) + 1, 1, 64)
+    with pytest.raises(ValueError):
+        q.op_rope(q.rope(64), many, pos)
 
 
 # --------------------------------------------------------------- together ----

@@ -158,3 +158,11 @@ def test_workspace_covers_fewer_rows():
         c = C.byref(_paged(**kw))
         sizes = [lib.qi21_attention_paged_bytes(c, n, 8) for n in (0, 1, 2, 7, 16, 17, 100, 1000, 1025, 5000)]
         assert sizes == sorted(sizes) and sizes[0] > 0
+
+
+def test_limits_of_lengths_and_scale():
+    lib = q.load()
+    c = C.byref(_paged(prefix_len=1 << 30))  # with the own rows 2^31 keys
+    assert lib.qi21_op_attention_paged(c, 4, 4, 256, 512, 256, 512, 1, None, 0.1, 256, 1 << 40, None) == -2
+    c = C.byref(_paged())
+    assert lib.qi21_op_attention_paged(c, 4, 4, 256, 512, 256, 512, 1, None, 2e38, 256, 1 << 40, None) == -1
