@@ -29,9 +29,10 @@ unsigned int rope_status_read_clear() {
 }
 
 constexpr int kRopeThreads = 256;
-// heads in flight per thread: 64 bytes of 16-byte pieces
+// heads of a thread's batch: 64 bytes of 16-byte pieces
 template <bool HALF>
 constexpr int kRopeBatch = HALF ? 2 : 4;
+constexpr int kRopeStages = 2;       // batches under way per thread (three: the same; four: one CTA an SM fewer, 83 us)
 constexpr int kRopeMaxCs = 4096;     // (cos, sin) pairs of a CTA: 32 KB
 constexpr int kRopeMaxRows = 64;     // rows of a CTA
 
@@ -47,6 +48,7 @@ struct RopeArgs {
   int units;       // of a head (see the kernel)
   int head_lanes;  // threads that share a row's column piece
   float sgn;       // -1 for the gradient
+  int cs_floats;   // of a CTA's (cos, sin)
   PagedArgs p;     // append only
 };
 
@@ -162,11 +164,14 @@ __device__ __forceinline__ void append_places(const PagedArgs& p, int row0, int 
 // in the HALF layout's turned part the two pieces whose values pair up. A
 // thread has one unit of every head_lanes-th head of a row (of the keys'
 // heads, then the values' in an append), so it reads the (cos, sin) of its
-// columns once per row and turns several heads with them. kRopeBatch heads
-// are loaded ahead of their arithmetic, the first ones ahead of the angles,
-// and four CTAs share an SM. What bounds it: the bytes of x and out. 32768
-// rows of 32 heads of 128 (bf16, 537 MB): 88 us, 6.1 TB/s; with (cos, sin)
-// read per head, conflicting banks and the frequencies read per angle, 118.
+// columns once per row and turns several heads with them. Its pieces of the
+// next two batches of heads are under way into a ring of its own in shared
+// memory (registers hold one batch only, and the SM then waits for memory
+// between its arithmetic: 88 us against 82 below), the first ones ahead of
+// the angles, and four CTAs share an SM. What bounds it: the bytes of x and
+// out. 32768 rows of 32 heads of 128 (bf16, 537 MB): 82 us, 6.6 TB/s, 97% of
+// a copy's rate; with (cos, sin) read per head, conflicting banks and the
+// frequencies read per angle, 118.
 template <typename T, bool HALF, int E, bool VECT, bool APPEND>
 __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_constant__ RopeArgs a) {
   extern __shared__ __align__(16) float cs[];  // [rpc][cos, sin][rot / 2]
@@ -194,8 +199,14 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
   const bool two = HALF && turns;
   const bool active = first < step;
 
+  // A thread's batches (NB heads of a row) follow each other by rows, then
+  // heads. 16-byte pieces go to a ring of the thread's own in shared memory,
+  // kRopeStages batches ahead; smaller ones to registers, one batch ahead
+  constexpr bool RING = VECT && sizeof(T) * E == 16;
+  constexpr int NP = HALF ? 2 * NB : NB;  // pieces of a batch
   P b0[NB], b1[NB];
-  auto load = [&](int row, int h0) {
+  uint4* ring = reinterpret_cast<uint4*>(cs + a.cs_floats) + tid;
+  auto load = [&](int row, int h0, int st) {
 #pragma unroll
     for (int k = 0; k < NB; ++k) {
       const int h = h0 + k * a.head_lanes;
@@ -203,12 +214,33 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
         const T* src = APPEND && h >= a.heads
                            ? static_cast<const T*>(a.v) + row * a.ldv + (h - a.heads) * a.dim + col
                            : static_cast<const T*>(a.x) + row * a.ldx + h * a.dim + col;
-        b0[k].load(src);
-        if (two) b1[k].load(src + hp);
+        if constexpr (RING) {
+          cp_async16(smem_u32(ring + (st * NP + k) * kRopeThreads), src);
+          if (two) cp_async16(smem_u32(ring + (st * NP + NB + k) * kRopeThreads), src + hp);
+        } else {
+          b0[k].load(src);
+          if (two) b1[k].load(src + hp);
+        }
       }
     }
   };
-  if (active && first < nrow) load(row0 + first, lane_h);
+  // the batch under way furthest ahead, and its stage
+  int fr = first, fh = lane_h;
+  auto fetch_next = [&](int st) {
+    if (active && fr < nrow) {
+      load(row0 + fr, fh, st);
+      fh += NB * a.head_lanes;
+      if (fh >= heads) {
+        fh = lane_h;
+        fr += step;
+      }
+    }
+    if constexpr (RING) cp_async_commit();
+  };
+  constexpr int ST = RING ? kRopeStages : 1;
+#pragma unroll
+  for (int k = 0; k < ST; ++k) fetch_next(k);
+  int st = 0;
 
   if (APPEND) {
     if (tid < 32) append_places(a.p, row0, nrow, tid, s_dst, s_pos);
@@ -286,7 +318,19 @@ __global__ void __launch_bounds__(kRopeThreads, 4) rope_kernel(const __grid_cons
       dst0 = static_cast<T*>(a.out) + (row0 + r) * a.ldo + col;
     }
     for (int h0 = lane_h; h0 < heads; h0 += NB * a.head_lanes) {
-      if (r != first || h0 != lane_h) load(row0 + r, h0);
+      if constexpr (RING) {
+        cp_async_wait<ST - 1>();
+#pragma unroll
+        for (int k = 0; k < NB; ++k) {
+          if (h0 + k * a.head_lanes >= heads) break;
+          *reinterpret_cast<uint4*>(b0[k].e) = ring[(st * NP + k) * kRopeThreads];
+          if (two) *reinterpret_cast<uint4*>(b1[k].e) = ring[(st * NP + NB + k) * kRopeThreads];
+        }
+        fetch_next(st);
+        if (++st == ST) st = 0;
+      } else if (r != first || h0 != lane_h) {
+        fetch_next(0);
+      }
 #pragma unroll
       for (int k = 0; k < NB; ++k) {
         const int h = h0 + k * a.head_lanes;
@@ -338,17 +382,28 @@ static cudaError_t launch_t(RopeArgs& a, bool inplace, cudaStream_t s) {
   const int lanes = a.rows < few ? heads : (heads + kRopeBatch<HALF> - 1) / kRopeBatch<HALF>;
   a.head_lanes = std::max(1, std::min(lanes, kRopeThreads / a.units));
   const int at_once = kRopeThreads / (a.units * a.head_lanes);
-  // rows of a CTA: four rounds of its threads, eight in an append, whose
-  // search for the rows' places is paid once per CTA (four images' rows: 27
-  // us against 29; a rotation of 32768 rows: 92 against 88), fewer while that
-  // would leave SMs idle, and no more than the (cos, sin) room
-  int64_t rpc = static_cast<int64_t>(at_once) * (APPEND ? 8 : 4);
+  // rows of a CTA: four rounds of its threads (a rotation of 36384 rows of 16
+  // heads: 48 us; eight rounds: 50, one: 58; an append of as many bytes: 51
+  // us, eight rounds: 53, sixteen: 60), fewer while that would leave SMs
+  // idle, and no more than the (cos, sin) room
+  int64_t rpc = static_cast<int64_t>(at_once) * 4;
   rpc = std::min<int64_t>(rpc, a.rows / few);
   if (hp > 0) rpc = std::min<int64_t>(rpc, kRopeMaxCs / hp);
   a.rpc = static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(rpc, kRopeMaxRows)));
   const unsigned grid = static_cast<unsigned>((a.rows + static_cast<int64_t>(a.rpc) - 1) / a.rpc);
-  rope_kernel<T, HALF, E, VECT, APPEND>
-      <<<grid, kRopeThreads, static_cast<size_t>(a.rpc) * hp * 2 * sizeof(float), s>>>(a);
+  a.cs_floats = (a.rpc * hp * 2 + 3) & ~3;
+  constexpr bool RING = VECT && sizeof(T) * E == 16;
+  constexpr int ring = RING ? kRopeStages * (HALF ? 2 : 1) * kRopeBatch<HALF> * kRopeThreads * 16 : 0;
+  if (RING) {
+    static PerDevice<cudaError_t> once;
+    const cudaError_t* attr = once.get([] {
+      return cudaFuncSetAttribute(rope_kernel<T, HALF, E, VECT, APPEND>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                  ring + kRopeMaxCs * 8);
+    });
+    if (attr == nullptr) return cudaErrorNoDevice;
+    if (*attr != cudaSuccess) return *attr;
+  }
+  rope_kernel<T, HALF, E, VECT, APPEND><<<grid, kRopeThreads, a.cs_floats * sizeof(float) + ring, s>>>(a);
   return cudaGetLastError();
 }
 

@@ -43,6 +43,16 @@ __device__ __forceinline__ int64_t paged_row(const PagedArgs& p, int b, int own,
   return -1;
 }
 
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+// 16 bytes from global to shared memory, both addresses multiples of 16.
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+
 constexpr float kPagedRescale = 8.0f;  // log2 units: p <= 2^8, in f16 range
 
 // One attention call over a paged cache.
