@@ -673,28 +673,6 @@ static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block
   return best;
 }
 
-// A launch that may start while the kernel before it in the stream runs
-// (grid_wait inside it).
-template <class... A>
-static cudaError_t launch_early(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
-                                unsigned cluster, const A&... args) {
-  cudaLaunchConfig_t cfg{};
-  cfg.gridDim = dim3(grid);
-  cfg.blockDim = dim3(threads);
-  cfg.dynamicSmemBytes = smem;
-  cfg.stream = s;
-  cudaLaunchAttribute at[2];
-  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  at[0].val.programmaticStreamSerializationAllowed = 1;
-  at[1].id = cudaLaunchAttributeClusterDimension;
-  at[1].val.clusterDim.x = cluster;
-  at[1].val.clusterDim.y = 1;
-  at[1].val.clusterDim.z = 1;
-  cfg.attrs = at;
-  cfg.numAttrs = cluster > 1 ? 2 : 1;
-  return cudaLaunchKernelEx(&cfg, kernel, args...);
-}
-
 template <bool BF, int D, int MT>
 static cudaError_t launch_narrow(const PagedAttnArgs& a, unsigned grid, unsigned cluster, cudaStream_t s) {
   constexpr int smem = kNarrowSmem<D, MT>;

@@ -132,6 +132,28 @@ __device__ __forceinline__ SeqTile warp_find_tile(const PagedAttnArgs& a, int x,
 __device__ __forceinline__ void grid_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 __device__ __forceinline__ void grid_release() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 
+// A launch that may start while the kernel before it in the stream runs
+// (grid_wait inside it).
+template <class... A>
+inline cudaError_t launch_early(void (*kernel)(A...), unsigned grid, unsigned threads, size_t smem, cudaStream_t s,
+                                unsigned cluster, const A&... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(grid);
+  cfg.blockDim = dim3(threads);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = s;
+  cudaLaunchAttribute at[2];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  at[1].id = cudaLaunchAttributeClusterDimension;
+  at[1].val.clusterDim.x = cluster;
+  at[1].val.clusterDim.y = 1;
+  at[1].val.clusterDim.z = 1;
+  cfg.attrs = at;
+  cfg.numAttrs = cluster > 1 ? 2 : 1;
+  return cudaLaunchKernelEx(&cfg, kernel, args...);
+}
+
 // Key `k` of [prefix, own rows] of a sequence: its K row of key head hk (the
 // V row is kv_heads * D further), or null for a page outside the cache.
 template <int D>

@@ -544,6 +544,64 @@ def test_captures_that_fork_and_that_start_with_a_call(case):
     assert torch.equal(o1, want) and torch.equal(o2, want) and torch.equal(o3, want + want)
 
 
+@pytest.mark.parametrize("case", [([1] * 6, [30] * 6, 100), ([300, 700, 90], [300, 800, 90], 400), ([2] * 40, [60] * 40, 6000)],
+                         ids=["small", "many", "parts"])
+def test_chains_of_calls_that_start_early(case):
+    # kernels that may start before the one ahead of them has ended: a chain
+    # in which each call reads what the one before wrote, against the same
+    # with the host waiting in between; eager, captured, and in two branches
+    counts, lens, prefix = case
+    b = P.Batch(counts, lens, prefix, 2, 128, 16, seed=50)
+    rng = np.random.default_rng(51)
+    x0 = dev(rng.standard_normal((b.rows, 12, 128)), torch.bfloat16)
+    pos = torch.arange(b.rows, device="cuda")
+    r = q.rope(128, layout="half")
+
+    class State:
+        def __init__(self):
+            self.pool = dev(b.pool, torch.bfloat16)
+            self.kv = _paged(b, self.pool)
+            self.x, self.out = x0.clone(), torch.zeros(b.rows, 8, 128, dtype=torch.bfloat16, device="cuda")
+            self.ws = torch.empty(q.attention_paged_bytes(self.kv, b.rows, 8), dtype=torch.uint8, device="cuda")
+
+        def run(self, wait=lambda: None, stream=None):
+            for i in range(3):
+                q.op_rope(r, self.x, pos, stream=stream)
+                wait()
+                q.op_kv_append(self.kv, self.x[:, 8:10], self.x[:, 10:], rope=r, stream=stream)
+                wait()
+                q.op_attention_paged(self.kv, self.x[:, :8], self.out, self.ws, stream=stream)
+                wait()
+                q.op_rope(r, self.out, pos, out=self.x[:, :8], grad=bool(i & 1), stream=stream)
+                wait()
+
+        def same(self, o):
+            return torch.equal(self.x, o.x) and torch.equal(self.out, o.out) and torch.equal(
+                self.pool.view(torch.int16), o.pool.view(torch.int16))
+
+    want = State()
+    want.run(torch.cuda.synchronize)
+    for _ in range(5):
+        got = State()
+        torch.cuda.synchronize()
+        got.run()
+        torch.cuda.synchronize()
+        assert got.same(want)
+    a, c = State(), State()
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        main, side = torch.cuda.current_stream(), torch.cuda.Stream()
+        side.wait_stream(main)
+        c.run(stream=side)
+        a.run()
+        main.wait_stream(side)
+        both = a.out + c.out
+    g.replay()
+    torch.cuda.synchronize()
+    assert a.same(want) and c.same(want) and torch.equal(both, want.out + want.out)
+
+
 def test_calls_of_two_streams_at_once():
     # two batches over one pool, each with its workspace, on streams that run
     # side by side
