@@ -639,15 +639,22 @@ size_t attn_paged_bytes(const PagedArgs& p, int rows, int heads) {
   return most * heads * (static_cast<size_t>(p.dim) * 4 + 8) + 256;
 }
 
+// The few-row tiles that run beside the tensor-core tiles, in microseconds:
+// their CTAs (three on an SM), one CTA's time, and the SM time of their bytes.
+struct Beside {
+  double ctas, each, sm_us;
+};
+
 // Parts of a wide call's keys: the count that ends first by a model in
 // microseconds. A CTA takes `fixed` to start and end and `per_block` for each
-// of its key blocks; the few-row tiles that run beside it take `beside`
-// SM-microseconds (their lengths are known to the device alone: half the
-// table's rows is assumed, so a count that makes the wide part itself 1.6
-// times longer than need be is out); a join takes 4 us (a call that is joined
-// anyway has it whatever the count), and parts are written and read back at
-// about 4 TB/s. Fewer parts pay `fixed` less often, more fill the GPU.
-static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block, bool joined, double beside,
+// of its key blocks. The few-row tiles beside take the SMs that it leaves;
+// those that are left over when it ends take a CTA's time more (their
+// lengths are known to the device alone: half the table's rows is assumed,
+// so a count that makes the wide part itself 1.6 times longer than need be
+// is out). A join takes 4 us (a call that is joined anyway has it whatever
+// the count), and parts are written and read back at about 4 TB/s. Fewer
+// parts pay `fixed` less often, more fill the GPU.
+static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block, bool joined, const Beside& few,
                        int64_t rows_heads, int dim, int most) {
   const double fixed = 8.0, sms = sm_count();
   double least = 0.0;
@@ -661,8 +668,14 @@ static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block
       if (pass == 0) {
         if (n == 1 || alone < least) least = alone;
       } else if (alone <= 1.6 * least) {
-        const double t = std::max(alone, (all * one + beside) / sms) +
-                         (n > 1 || joined ? 4.0 + n * static_cast<double>(rows_heads) * dim * 8 / 4e6 : 0.0);
+        double t = std::max(alone, (all * one + few.sm_us) / sms);
+        if (few.ctas > 0.0) {
+          const double slots = 3.0 * std::max(0.0, sms - all);  // beside
+          const double late = few.ctas - slots * (std::floor(alone / few.each) + 1.0);
+          t = std::max(t, late > 0.0 ? alone + few.each * std::max(1.0, late / (3.0 * sms))
+                                     : few.each * std::ceil(few.ctas / slots));
+        }
+        if (n > 1 || joined) t += 4.0 + n * static_cast<double>(rows_heads) * dim * 8 / 4e6;
         if (got == 0.0 || t < got) {
           got = t;
           best = n;
@@ -722,7 +735,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     const int per = tokens * (pair ? 2 : 1);
     const int64_t tiles = a.rows / per + seqs;
     if (tiles > 0x3fffffff / kMaxSlots) return cudaErrorInvalidValue;
-    a.slots = stay ? 1 : wide_splits(items(pair), pair ? 2 : 1, blocks, block_us(pair), false, 0.0, all, D, most);
+    a.slots = stay ? 1 : wide_splits(items(pair), pair ? 2 : 1, blocks, block_us(pair), false, Beside{0, 0, 0}, all, D, most);
     place_parts();
     e = launch_attn_wide(a, stay ? WIDE_STAY : WIDE_JOINT, pair, static_cast<int>(tiles), a.slots, s);
     return e != cudaSuccess || a.slots == 1 ? e : join();
@@ -739,12 +752,18 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   };
   const int64_t own_tiles = pairs / R + seqs;
   a.own_tiles = static_cast<int>(own_tiles);
-  // a small call: one launch in which every sequence reads the prefix itself
+  // a small call: one launch in which every sequence reads the prefix itself,
+  // while its CTAs have so few keys each that parts and their join take
+  // longer (one sequence, 8 key heads, 2000 keys: 8.9 us against 9.1, 4000:
+  // 12.0 against 9.4). Where SMs have several CTAs that is sooner if a prefix
+  // is then read once (two sequences behind 1000 keys, 32 key heads: 10.8
+  // against 9.4), later if not (one of 4000 keys: 14.1 against 16.6)
   const double again = static_cast<double>(own_tiles) * hk * P * (4 * D);  // bytes of that
   const int64_t keys = static_cast<int64_t>(P) + a.kv.table_rows;
   int64_t ncl = std::min<int64_t>(3 * static_cast<int64_t>(sm_count()) / (own_tiles * hk), keys / 64);
   ncl = ncl >= 8 ? 8 : ncl >= 4 ? 4 : ncl >= 2 ? 2 : 1;
-  if (again <= kReadAgain && keys <= 1024 * ncl && own_tiles * hk * ncl <= 0x7fffffff) {
+  const int64_t each_most = ncl == 1 ? 1024 : own_tiles * hk * ncl <= sm_count() ? 384 : P > 0 ? 256 : 640;
+  if (again <= kReadAgain && keys <= each_most * ncl && own_tiles * hk * ncl <= 0x7fffffff) {
     a.cluster = static_cast<int>(ncl);
     a.own_splits = 1;
     a.slots = 1;
@@ -762,16 +781,22 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     return static_cast<int>(n);
   };
   // bytes that few-row tiles of the prefix read
-  const double few = static_cast<double>((pairs + R - 1) / R) * P * hk * (4 * D);
-  const bool wide = P > 0 && tokens > 0 && pairs > R && few > kFewRowPrefix;
+  const double again_few = static_cast<double>((pairs + R - 1) / R) * P * hk * (4 * D);
+  const bool wide = P > 0 && tokens > 0 && pairs > R && again_few > kFewRowPrefix;
   const bool pair = D == 128 && pairs > 128;
   const int per = tokens * (pair ? 2 : 1);
   int wide_tiles = 0;
   if (wide) {
     wide_tiles = (a.rows + per - 1) / per;
-    const double own_bytes = 0.5 * seqs * a.kv.table_rows * hk * (4.0 * D);
+    // a few-row CTA takes 4 us to start and end and 0.95 per 64 keys
+    const double half = 0.5 * a.kv.table_rows;
+    const int cut = splits(a.own_tiles, a.kv.table_rows, most - 1, &a.own_keys);
+    const double keys_each = std::max(half / cut, std::min(half, 256.0));
+    const int64_t each = (a.rows + static_cast<int64_t>(seqs) - 1) / seqs;
+    const Beside few{static_cast<double>(seqs * ((each * a.group + R - 1) / R) * hk) * std::ceil(half / keys_each),
+                     4.0 + 0.95 * keys_each / 64, half * seqs * hk * (4.0 * D) / 30e3};
     a.pre_splits = wide_splits(static_cast<int64_t>(wide_tiles) * hk, pair ? 2 : 1, (static_cast<int64_t>(P) + 127) / 128,
-                               block_us(pair), true, own_bytes / 30e3, all, D, most - 1);
+                               block_us(pair), true, few, all, D, most - 1);
   } else if (P > 0) {
     a.pre_tiles = static_cast<int>((pairs + R - 1) / R);
     a.pre_splits = splits(a.pre_tiles, P, most - 1, &a.pre_keys);
