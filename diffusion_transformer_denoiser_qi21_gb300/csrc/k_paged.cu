@@ -31,6 +31,7 @@ constexpr int kWarps = 4;               // of a CTA
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src, bool live) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(live ? 16 : 0) : "memory");
 }
+
 // Loads from the shared memory of a CTA of the cluster.
 __device__ __forceinline__ float2 ld_cluster2(uint32_t addr) {
   float2 v;
@@ -627,8 +628,8 @@ constexpr int kMaxSlots = 128;
 // Bytes of the prefix that a small call may read once per sequence instead
 // of once for all, and that few-row tiles of all rows may read instead of the
 // tensor-core tiles, which take some 8 us to start and end (8 sequences of 4
-// heads behind 2000 rows, 8 key heads: 12.4 us against 16.4; behind 8000:
-// 20.6 against 16.4).
+// heads behind 2000 rows, 8 key heads: 10.9 us against 13.0; behind 8000:
+// 19.0 against 13.9).
 constexpr int64_t kReadAgain = 32 << 20;
 constexpr int64_t kFewRowPrefix = 24 << 20;
 static int paged_slots(int rows) { return std::min(kMaxSlots, std::max(2, kPartRows / std::max(1, rows))); }
