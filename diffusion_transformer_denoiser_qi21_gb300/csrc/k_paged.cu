@@ -687,6 +687,34 @@ static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block
   return best;
 }
 
+// Parts of the own keys of a call without a prefix, `tiles` few-row tiles of
+// `keys` keys, `of_seq` of them with the same keys: the count that ends first
+// by a model in microseconds. 64 keys take a CTA 0.95, or their share of 6.6
+// TB/s among the CTAs that run with it (`per_sm` on an SM; tiles with the
+// same keys find them in the L2), both slowing it where they are alike. A
+// CTA takes 2.3 more to start and end beside others, 3.5 in the last wave,
+// which also waits for its slowest SM the fuller it is. (300 sequences of
+// 2000 keys, one key head: one part 53 us, three 62; 64 of them: five parts
+// 15.9, eight 20; one of 60000 keys, 8 key heads: 114 parts 49, 57 54.)
+static int own_parts(int64_t tiles, int64_t of_seq, int64_t keys, int dim, int per_sm, int64_t rows_heads, int most) {
+  const double slots = static_cast<double>(per_sm) * sm_count(), alone = 0.95 / 64;
+  auto share = [&](double ctas) { return ctas * (4 * dim) / 6.6e6 / std::min<double>(static_cast<double>(of_seq), 3.0); };
+  double got = 0.0;
+  int best = 1;
+  for (int n = 1; n <= most && (n == 1 || keys >= 256 * static_cast<int64_t>(n)); ++n) {
+    const double each = static_cast<double>(keys) / n, all = static_cast<double>(tiles) * n;
+    const double full = std::ceil(all / slots) - 1.0, last = all - full * slots;
+    const double key = std::sqrt(std::hypot(alone * alone, share(last) * share(last))) * (1.0 + 0.2 * std::pow(last / slots, 4));
+    const double t = full * (2.3 + each * std::max(alone, share(slots))) + 3.5 + each * key +
+                     (n > 1 ? 4.0 + n * static_cast<double>(rows_heads) * dim * 8 / 4e6 : 0.0);
+    if (n == 1 || t < got) {
+      got = t;
+      best = n;
+    }
+  }
+  return best;
+}
+
 template <bool BF, int D, int MT>
 static cudaError_t launch_narrow(const PagedAttnArgs& a, unsigned grid, unsigned cluster, cudaStream_t s) {
   constexpr int smem = kNarrowSmem<D, MT>;
@@ -786,6 +814,8 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   const bool wide = P > 0 && tokens > 0 && pairs > R && again_few > kFewRowPrefix;
   const bool pair = D == 128 && pairs > 128;
   const int per = tokens * (pair ? 2 : 1);
+  const int64_t each = (a.rows + static_cast<int64_t>(seqs) - 1) / seqs;
+  const int64_t of_seq = (each * a.group + R - 1) / R, live = seqs * of_seq * hk;  // few-row tiles, the rows shared evenly
   int wide_tiles = 0;
   if (wide) {
     wide_tiles = (a.rows + per - 1) / per;
@@ -793,8 +823,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     const double half = 0.5 * a.kv.table_rows;
     const int cut = splits(a.own_tiles, a.kv.table_rows, most - 1, &a.own_keys);
     const double keys_each = std::max(half / cut, std::min(half, 256.0));
-    const int64_t each = (a.rows + static_cast<int64_t>(seqs) - 1) / seqs;
-    const Beside few{static_cast<double>(seqs * ((each * a.group + R - 1) / R) * hk) * std::ceil(half / keys_each),
+    const Beside few{static_cast<double>(live) * std::ceil(half / keys_each),
                      4.0 + 0.95 * keys_each / 64, half * seqs * hk * (4.0 * D) / 30e3};
     a.pre_splits = wide_splits(static_cast<int64_t>(wide_tiles) * hk, pair ? 2 : 1, (static_cast<int64_t>(P) + 127) / 128,
                                block_us(pair), true, few, all, D, most - 1);
@@ -802,7 +831,12 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     a.pre_tiles = static_cast<int>((pairs + R - 1) / R);
     a.pre_splits = splits(a.pre_tiles, P, most - 1, &a.pre_keys);
   }
-  a.own_splits = splits(a.own_tiles, a.kv.table_rows, most - a.pre_splits, &a.own_keys);
+  if (P > 0) {
+    a.own_splits = splits(a.own_tiles, a.kv.table_rows, most - a.pre_splits, &a.own_keys);
+  } else {
+    a.own_splits = own_parts(live, of_seq, a.kv.table_rows, D, two ? 2 : D == 128 ? 3 : 4, all, most);
+    a.own_keys = static_cast<int>((static_cast<int64_t>(a.kv.table_rows) + a.own_splits - 1) / a.own_splits + kGran - 1) / kGran * kGran;
+  }
   a.slots = a.pre_splits + a.own_splits;
   place_parts();
   const int64_t gx = hk * (static_cast<int64_t>(a.pre_tiles) * a.pre_splits +
