@@ -689,20 +689,21 @@ static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block
 
 // Parts of the own keys of a call without a prefix, `tiles` few-row tiles of
 // `keys` keys, `of_seq` of them with the same keys: the count that ends first
-// by a model in microseconds. 64 keys take a CTA 0.95, or their share of 6.6
+// by a model in microseconds. 64 keys (a granule of each warp) take a CTA
+// 0.95, or their share of 6.6
 // TB/s among the CTAs that run with it (`per_sm` on an SM; tiles with the
 // same keys find them in the L2), both slowing it where they are alike. A
 // CTA takes 2.3 more to start and end beside others, 3.5 in the last wave,
 // which also waits for its slowest SM the fuller it is. (300 sequences of
 // 2000 keys, one key head: one part 53 us, three 62; 64 of them: five parts
 // 15.9, eight 20; one of 60000 keys, 8 key heads: 114 parts 49, 57 54.)
-static int own_parts(int64_t tiles, int64_t of_seq, int64_t keys, int dim, int per_sm, int64_t rows_heads, int most) {
+static int few_row_parts(int64_t tiles, int64_t of_seq, int64_t keys, int dim, int per_sm, int64_t rows_heads, int most) {
   const double slots = static_cast<double>(per_sm) * sm_count(), alone = 0.95 / 64;
   auto share = [&](double ctas) { return ctas * (4 * dim) / 6.6e6 / std::min<double>(static_cast<double>(of_seq), 3.0); };
   double got = 0.0;
   int best = 1;
-  for (int n = 1; n <= most && (n == 1 || keys >= 256 * static_cast<int64_t>(n)); ++n) {
-    const double each = static_cast<double>(keys) / n, all = static_cast<double>(tiles) * n;
+  for (int n = 1; n <= most && (n == 1 || keys > 256 * static_cast<int64_t>(n - 1)); ++n) {
+    const double each = 64.0 * std::ceil(static_cast<double>(keys) / (64.0 * n)), all = static_cast<double>(tiles) * n;
     const double full = std::ceil(all / slots) - 1.0, last = all - full * slots;
     const double key = std::sqrt(std::hypot(alone * alone, share(last) * share(last))) * (1.0 + 0.2 * std::pow(last / slots, 4));
     const double t = full * (2.3 + each * std::max(alone, share(slots))) + 3.5 + each * key +
@@ -803,10 +804,12 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
   // sequence's own keys for its own. Parts of the few-row tiles: enough CTAs
   // for two waves of three per SM, none of fewer than 256 keys
   const int64_t want = 6 * static_cast<int64_t>(sm_count());
+  const int per_sm = two ? 2 : D == 128 ? 3 : 4;  // few-row CTAs on an SM
+  auto part_keys = [](int64_t keys, int64_t n) { return static_cast<int>(((keys + n - 1) / n + kGran - 1) / kGran * kGran); };
   auto splits = [&](int64_t tiles, int64_t keys, int cap, int* part) {
     int64_t n = std::min<int64_t>((want + tiles * hk - 1) / (tiles * hk), (keys + 255) / 256);
     n = std::max<int64_t>(1, std::min<int64_t>(n, cap));
-    *part = static_cast<int>(((keys + n - 1) / n + kGran - 1) / kGran * kGran);
+    *part = part_keys(keys, n);
     return static_cast<int>(n);
   };
   // bytes that few-row tiles of the prefix read
@@ -829,13 +832,14 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
                                block_us(pair), true, few, all, D, most - 1);
   } else if (P > 0) {
     a.pre_tiles = static_cast<int>((pairs + R - 1) / R);
-    a.pre_splits = splits(a.pre_tiles, P, most - 1, &a.pre_keys);
+    a.pre_splits = few_row_parts(static_cast<int64_t>(a.pre_tiles) * hk, a.pre_tiles, P, D, per_sm, all, most - 1);
+    a.pre_keys = part_keys(P, a.pre_splits);
   }
   if (P > 0) {
     a.own_splits = splits(a.own_tiles, a.kv.table_rows, most - a.pre_splits, &a.own_keys);
   } else {
-    a.own_splits = own_parts(live, of_seq, a.kv.table_rows, D, two ? 2 : D == 128 ? 3 : 4, all, most);
-    a.own_keys = static_cast<int>((static_cast<int64_t>(a.kv.table_rows) + a.own_splits - 1) / a.own_splits + kGran - 1) / kGran * kGran;
+    a.own_splits = few_row_parts(live, of_seq, a.kv.table_rows, D, per_sm, all, most);
+    a.own_keys = part_keys(a.kv.table_rows, a.own_splits);
   }
   a.slots = a.pre_splits + a.own_splits;
   place_parts();
