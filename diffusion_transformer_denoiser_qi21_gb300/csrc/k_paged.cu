@@ -687,17 +687,18 @@ static int wide_splits(int64_t items, int ctas, int64_t blocks, double per_block
   return best;
 }
 
-// Parts of the own keys of a call without a prefix, `tiles` few-row tiles of
-// `keys` keys, `of_seq` of them with the same keys: the count that ends first
-// by a model in microseconds. 64 keys (a granule of each warp) take a CTA
-// 0.95, or their share of 6.6
+// Parts of the keys of `tiles` few-row tiles of `keys` keys, `of_seq` of them
+// with the same keys: the count that ends first by a model in microseconds.
+// 64 keys (a granule of each warp) take a CTA 0.95, or their share of 6.6
 // TB/s among the CTAs that run with it (`per_sm` on an SM; tiles with the
 // same keys find them in the L2), both slowing it where they are alike. A
 // CTA takes 2.3 more to start and end beside others, 3.5 in the last wave,
-// which also waits for its slowest SM the fuller it is. (300 sequences of
-// 2000 keys, one key head: one part 53 us, three 62; 64 of them: five parts
-// 15.9, eight 20; one of 60000 keys, 8 key heads: 114 parts 49, 57 54.)
-static int few_row_parts(int64_t tiles, int64_t of_seq, int64_t keys, int dim, int per_sm, int64_t rows_heads, int most) {
+// which also waits for its slowest SM, the fuller it is the longer. (300
+// sequences of 2000 keys, one key head: one part 53 us, three 62; 64 of them:
+// five parts 15.9, eight 20; two of 60000, 32 key heads: 279, as two waves of
+// CTAs of like length 320.)
+static int few_row_parts(int64_t tiles, int64_t of_seq, int64_t keys, int dim, int per_sm, bool joined,
+                         int64_t rows_heads, int most) {
   const double slots = static_cast<double>(per_sm) * sm_count(), alone = 0.95 / 64;
   auto share = [&](double ctas) { return ctas * (4 * dim) / 6.6e6 / std::min<double>(static_cast<double>(of_seq), 3.0); };
   double got = 0.0;
@@ -707,7 +708,7 @@ static int few_row_parts(int64_t tiles, int64_t of_seq, int64_t keys, int dim, i
     const double full = std::ceil(all / slots) - 1.0, last = all - full * slots;
     const double key = std::sqrt(std::hypot(alone * alone, share(last) * share(last))) * (1.0 + 0.2 * std::pow(last / slots, 4));
     const double t = full * (2.3 + each * std::max(alone, share(slots))) + 3.5 + each * key +
-                     (n > 1 ? 4.0 + n * static_cast<double>(rows_heads) * dim * 8 / 4e6 : 0.0);
+                     (n > 1 || joined ? 4.0 + n * static_cast<double>(rows_heads) * dim * 8 / 4e6 : 0.0);
     if (n == 1 || t < got) {
       got = t;
       best = n;
@@ -801,16 +802,15 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     return narrow(own_tiles * hk * ncl, ncl);
   }
   // few rows per sequence: the prefix for the rows of all sequences, each
-  // sequence's own keys for its own. Parts of the few-row tiles: enough CTAs
-  // for two waves of three per SM, none of fewer than 256 keys
-  const int64_t want = 6 * static_cast<int64_t>(sm_count());
+  // sequence's own keys for its own
   const int per_sm = two ? 2 : D == 128 ? 3 : 4;  // few-row CTAs on an SM
   auto part_keys = [](int64_t keys, int64_t n) { return static_cast<int>(((keys + n - 1) / n + kGran - 1) / kGran * kGran); };
-  auto splits = [&](int64_t tiles, int64_t keys, int cap, int* part) {
-    int64_t n = std::min<int64_t>((want + tiles * hk - 1) / (tiles * hk), (keys + 255) / 256);
-    n = std::max<int64_t>(1, std::min<int64_t>(n, cap));
-    *part = part_keys(keys, n);
-    return static_cast<int>(n);
+  // of the own keys beside tensor-core tiles: CTAs for two waves of three per
+  // SM, none of fewer than 256 keys
+  auto beside_parts = [&](int cap) {
+    const int64_t n = std::min<int64_t>((6 * static_cast<int64_t>(sm_count()) + own_tiles * hk - 1) / (own_tiles * hk),
+                                        (static_cast<int64_t>(a.kv.table_rows) + 255) / 256);
+    return static_cast<int>(std::max<int64_t>(1, std::min<int64_t>(n, cap)));
   };
   // bytes that few-row tiles of the prefix read
   const double again_few = static_cast<double>((pairs + R - 1) / R) * P * hk * (4 * D);
@@ -824,7 +824,7 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
     wide_tiles = (a.rows + per - 1) / per;
     // a few-row CTA takes 4 us to start and end and 0.95 per 64 keys
     const double half = 0.5 * a.kv.table_rows;
-    const int cut = splits(a.own_tiles, a.kv.table_rows, most - 1, &a.own_keys);
+    const int cut = beside_parts(most - 1);
     const double keys_each = std::max(half / cut, std::min(half, 256.0));
     const Beside few{static_cast<double>(live) * std::ceil(half / keys_each),
                      4.0 + 0.95 * keys_each / 64, half * seqs * hk * (4.0 * D) / 30e3};
@@ -832,15 +832,12 @@ static cudaError_t launch_paged_t(PagedAttnArgs& a, cudaStream_t s) {
                                block_us(pair), true, few, all, D, most - 1);
   } else if (P > 0) {
     a.pre_tiles = static_cast<int>((pairs + R - 1) / R);
-    a.pre_splits = few_row_parts(static_cast<int64_t>(a.pre_tiles) * hk, a.pre_tiles, P, D, per_sm, all, most - 1);
+    a.pre_splits = few_row_parts(static_cast<int64_t>(a.pre_tiles) * hk, a.pre_tiles, P, D, per_sm, true, all, most - 1);
     a.pre_keys = part_keys(P, a.pre_splits);
   }
-  if (P > 0) {
-    a.own_splits = splits(a.own_tiles, a.kv.table_rows, most - a.pre_splits, &a.own_keys);
-  } else {
-    a.own_splits = few_row_parts(live, of_seq, a.kv.table_rows, D, per_sm, all, most);
-    a.own_keys = part_keys(a.kv.table_rows, a.own_splits);
-  }
+  a.own_splits = wide ? beside_parts(most - a.pre_splits)
+                      : few_row_parts(live, of_seq, a.kv.table_rows, D, per_sm, P > 0, all, most - a.pre_splits);
+  a.own_keys = part_keys(a.kv.table_rows, a.own_splits);
   a.slots = a.pre_splits + a.own_splits;
   place_parts();
   const int64_t gx = hk * (static_cast<int64_t>(a.pre_tiles) * a.pre_splits +
